@@ -80,6 +80,11 @@ typedef enum tq_status {
 #define TQ_FLAG_INPUTS_READY (1u << 6)       /* see "Launch overlap" below                      */
 #define TQ_FLAG_ACCUMULATE (1u << 9)         /* tq_ternary_backward_input: dX += result         */
 #define TQ_FLAG_SHARED_INPUT (1u << 10)      /* tq_bitlinear_grouped: one x for all G layers    */
+#define TQ_FLAG_NORM_TOPK (1u << 11)         /* tq_moe_swiglu: weights add up to 1 per token    */
+#define TQ_FLAG_FP8_SQUARE (1u << 12)        /* tq_quantize_fp8: 128 x 128 blocks               */
+#define TQ_FLAG_FP8_W_ROWS (1u << 13)        /* tq_fp8_gemm: w has a scale per row and block    */
+#define TQ_FLAG_BF16_INPUT (1u << 14)        /* tq_quantize_fp8: x is bf16                      */
+#define TQ_FLAG_BF16_OUTPUT (1u << 15)       /* tq_fp8_gemm: y is bf16                          */
 
 /* Packed-code layout (flag bits 7-8; tq_quantize_ternary_pack[_noalloc],
  * tq_ternary_gemm, tq_bitlinear_fused).  Four codes per byte, LSB first.
@@ -362,6 +367,67 @@ TQ_API tq_status tq_swiglu_mlp(const float *x, int64_t M, int64_t d_model, int64
                                const float *down_gamma, float *y, float *act_out, void *workspace,
                                size_t workspace_bytes, tq_stream_t stream);
 TQ_API size_t tq_swiglu_workspace_bytes(int64_t M, int64_t d_model, int64_t d_ffn, unsigned flags);
+
+/*
+ * Quantisation to 8-bit floating point (e4m3) with one fp32 scale per block of
+ * 128, for the layers that a network keeps out of ternary (tq_fp8_gemm):
+ *
+ *   s = max(max |x| over the block, 1e-20) / 448,  q = e4m3(fp32(x / s))
+ *
+ * (IEEE fp32 divisions; half to even; the largest element of a block becomes
+ * +-448, e4m3's largest value.)
+ *
+ *   x         [rows][cols] fp32, or bf16 with TQ_FLAG_BF16_INPUT; read once
+ *             (twice with TQ_FLAG_RMSNORM).  1 <= rows, cols <= 2^24; neither
+ *             needs to be a multiple of anything.
+ *   flags     none: 1 x 128 blocks along each row.  TQ_FLAG_FP8_SQUARE: 128 x 128
+ *             blocks (weights).  TQ_FLAG_RMSNORM (1 x 128 without qt only): the
+ *             row is first normalised, x * rsqrt(mean x^2 + rms_eps) * rms_gain,
+ *             as in tq_bitlinear_fused (rms_gain [cols] fp32, or NULL for 1).
+ *   q         [rows][ld], ld = tq_fp8_row_bytes(cols) = cols rounded up to 16;
+ *             the bytes past cols are written as zeros.
+ *   s         fp32: [ceil(cols/128)][rows] (a block's scales of all rows are
+ *             consecutive), or [ceil(rows/128)][ceil(cols/128)] with
+ *             TQ_FLAG_FP8_SQUARE.
+ *   qt, st    both NULL, or the codes and scales of x transposed, as this call
+ *             would give them for a [cols][rows] matrix: qt [cols]
+ *             [tq_fp8_row_bytes(rows)] with its own blocks along the rows of x,
+ *             st [ceil(rows/128)][cols] (square: the same codes transposed, st
+ *             [ceil(cols/128)][ceil(rows/128)]).  The operands of a product over
+ *             the rows of x: a weight or input gradient.
+ * Every pointer 16-byte aligned; outputs overlap nothing.  A NaN gives a NaN
+ * code; an infinity makes its block's other codes 0 and its own NaN.
+ */
+TQ_API tq_status tq_quantize_fp8(const void *x, int64_t rows, int64_t cols, unsigned flags, const float *rms_gain,
+                                 float rms_eps, uint8_t *q, float *s, uint8_t *qt, float *st, tq_stream_t stream);
+
+/* Bytes of one row of K codes as tq_quantize_fp8 writes and tq_fp8_gemm reads it. */
+TQ_API size_t tq_fp8_row_bytes(int64_t K);
+
+/*
+ * Product of e4m3 operands with a scale per block of 128 along K:
+ *
+ *   y[m][n] = sum_b s_x[b][m] * s_w(n, b) * sum_{k in block b} xq[m][k] * wq[n][k]
+ *
+ *   xq, s_x   [M][ld] codes, ld = tq_fp8_row_bytes(K), and [ceil(K/128)][M]
+ *             scales, as tq_quantize_fp8 writes them for an [M][K] matrix.
+ *   wq, s_w   [N][ld] codes and [ceil(N/128)][ceil(K/128)] scales
+ *             (TQ_FLAG_FP8_SQUARE's layout), or with TQ_FLAG_FP8_W_ROWS
+ *             [ceil(K/128)][N] scales (1 x 128 blocks).
+ *   y         [M][N] fp32, written; bf16 with TQ_FLAG_BF16_OUTPUT; fp32 and
+ *             added to with TQ_FLAG_ACCUMULATE.
+ *   flags     the above and TQ_FLAG_WEIGHTS_STATIC (see "Launch overlap").
+ *   Shapes: 1 <= M, N, K <= 2^24.
+ * A block's products (exact) and the blocks' scaled sums are added in fp32; the
+ * result is a function of the arguments alone (no atomics).  For the layer
+ * y = x w^T of a training step with x [M][K], w [N][K], dy [M][N]:
+ *   y  = (x rows)  . (w square)          K  = K
+ *   dx = (dy rows) . (w square)^T        the square form's qt, st;  K = N
+ *   dw = (dy)^T . x: the row form's qt, st of dy, and those of x with
+ *        TQ_FLAG_FP8_W_ROWS;  M = N, N = K, K = M.
+ */
+TQ_API tq_status tq_fp8_gemm(const uint8_t *xq, const float *s_x, const uint8_t *wq, const float *s_w, unsigned flags,
+                             int64_t M, int64_t N, int64_t K, void *y, tq_stream_t stream);
 
 /*
  * Grouped small-M layer: G independent layers of one shape (N x K, packed

@@ -31,6 +31,11 @@ ENC_FORMAT1 = 2 << 7
 ENC_MASK = 3 << 7
 FLAG_ACCUMULATE = 1 << 9  # tq_ternary_backward_input: dX += result
 FLAG_SHARED_INPUT = 1 << 10  # tq_bitlinear_grouped: one activation batch for all layers
+FLAG_NORM_TOPK = 1 << 11  # tq_moe_swiglu: a token's weights add up to 1
+FLAG_FP8_SQUARE = 1 << 12  # tq_quantize_fp8: 128 x 128 blocks
+FLAG_FP8_W_ROWS = 1 << 13  # tq_fp8_gemm: w has a scale per row and block
+FLAG_BF16_INPUT = 1 << 14  # tq_quantize_fp8: x is bf16
+FLAG_BF16_OUTPUT = 1 << 15  # tq_fp8_gemm: y is bf16
 
 STATUS = {0: "TQ_OK", 1: "TQ_ERR_NULL", 2: "TQ_ERR_SHAPE", 3: "TQ_ERR_ALIGN", 4: "TQ_ERR_ARG",
           5: "TQ_ERR_CUDA", 6: "TQ_ERR_DEVICE", 7: "TQ_ERR_TIMEOUT"}
@@ -56,6 +61,9 @@ SIGNATURES = {
     "tq_swiglu_workspace_bytes": (_SZ, [_I64, _I64, _I64, _U]),
     "tq_bitlinear_grouped": (_I, [_P, _I64, _P, _P, _U, _I64, _I64, _I64, _P, _P, _SZ, _P]),
     "tq_grouped_workspace_bytes": (_SZ, [_I64, _I64, _I64, _U]),
+    "tq_quantize_fp8": (_I, [_P, _I64, _I64, _U, _P, _F, _P, _P, _P, _P, _P]),
+    "tq_fp8_row_bytes": (_SZ, [_I64]),
+    "tq_fp8_gemm": (_I, [_P, _P, _P, _P, _U, _I64, _I64, _I64, _P, _P]),
     "tq_ternary_backward_input": (_I, [_P, _P, _P, _P, _U, _I64, _I64, _I64, _P, _P, _SZ, _P]),
     "tq_backward_input_workspace_bytes": (_SZ, [_I64, _I64]),
     "tq_ste_backward": (_I, [_P, _P, _P, _I64, _I64, _F, _U, _P, _P]),
@@ -337,6 +345,49 @@ def swiglu_mlp_(x, gate, up, down, flags, y, workspace, clamp_val=10.0, act_out=
                                 _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
+def fp8_row_bytes(K: int) -> int:
+    """Bytes of a row of K e4m3 codes: K rounded up to 16."""
+    return (K + 15) // 16 * 16
+
+
+def quantize_fp8_(x, flags, q, s, qt=None, st=None, rms_gain=None, rms_eps=1e-6, stream=None):
+    """x [R, C] float32 (bfloat16 with FLAG_BF16_INPUT); q [R, fp8_row_bytes(C)]
+    float8_e4m3fn; s [ceil(C/128), R], or [ceil(R/128), ceil(C/128)] with
+    FLAG_FP8_SQUARE; qt, st: the same for the transpose of x, or None."""
+    import torch
+
+    R, C = x.shape
+    rb, cb = -(-R // 128), -(-C // 128)
+    square = bool(flags & FLAG_FP8_SQUARE)
+    f8 = torch.float8_e4m3fn
+    _need(x, torch.bfloat16 if flags & FLAG_BF16_INPUT else torch.float32, (R, C), "x")
+    _need(q, f8, (R, fp8_row_bytes(C)), "q")
+    _need(s, torch.float32, (rb, cb) if square else (cb, R), "s")
+    _need(qt, f8, (C, fp8_row_bytes(R)), "qt")
+    _need(st, torch.float32, (cb, rb) if square else (rb, C), "st")
+    _need(rms_gain, torch.float32, (C,), "rms_gain")
+    _check("tq_quantize_fp8",
+           load().tq_quantize_fp8(_ptr(x), R, C, flags, _ptr(rms_gain), float(rms_eps), _ptr(q), _ptr(s), _ptr(qt),
+                                  _ptr(st), _stream(stream)))
+
+
+def fp8_gemm_(xq, s_x, wq, s_w, K, flags, y, stream=None):
+    """xq [M, fp8_row_bytes(K)], wq [N, fp8_row_bytes(K)] float8_e4m3fn; s_x
+    [ceil(K/128), M]; s_w [ceil(N/128), ceil(K/128)], or [ceil(K/128), N] with
+    FLAG_FP8_W_ROWS; y [M, N] float32, or bfloat16 with FLAG_BF16_OUTPUT."""
+    import torch
+
+    M, N, ld, kb = xq.shape[0], wq.shape[0], fp8_row_bytes(K), -(-K // 128)
+    f8 = torch.float8_e4m3fn
+    _need(xq, f8, (M, ld), "xq")
+    _need(wq, f8, (N, ld), "wq")
+    _need(s_x, torch.float32, (kb, M), "s_x")
+    _need(s_w, torch.float32, (kb, N) if flags & FLAG_FP8_W_ROWS else (-(-N // 128), kb), "s_w")
+    _need(y, torch.bfloat16 if flags & FLAG_BF16_OUTPUT else torch.float32, (M, N), "y")
+    _check("tq_fp8_gemm",
+           load().tq_fp8_gemm(_ptr(xq), _ptr(s_x), _ptr(wq), _ptr(s_w), flags, M, N, K, _ptr(y), _stream(stream)))
+
+
 def backward_input_workspace_bytes(M: int, N: int) -> int:
     return load().tq_backward_input_workspace_bytes(M, N)
 
@@ -469,3 +520,29 @@ def bitlinear_fused(x, packed, gamma, per_row: bool, rmsnorm: bool = True, fwht:
     bitlinear_fused_(x, packed, gamma, flags, y, ws, rms_gain, rms_eps, eta_min, eta_max, xq, sx,
                      stream)
     return (y, xq, sx) if return_xq else y
+
+
+def quantize_fp8(x, square: bool = False, transpose: bool = False, rmsnorm: bool = False, rms_gain=None,
+                 rms_eps: float = 1e-6, stream=None):
+    """(q, s) of x [R, C] (float32 or bfloat16), or (q, s, qt, st) with `transpose`."""
+    import torch
+
+    R, C = x.shape
+    rb, cb = -(-R // 128), -(-C // 128)
+    flags = ((FLAG_FP8_SQUARE if square else 0) | (FLAG_RMSNORM if rmsnorm else 0) |
+             (FLAG_BF16_INPUT if x.dtype == torch.bfloat16 else 0))
+    new = lambda shape, dt: torch.empty(shape, dtype=dt, device=x.device)  # noqa: E731
+    out = [new((R, fp8_row_bytes(C)), torch.float8_e4m3fn), new((rb, cb) if square else (cb, R), torch.float32)]
+    if transpose:
+        out += [new((C, fp8_row_bytes(R)), torch.float8_e4m3fn), new((cb, rb) if square else (rb, C), torch.float32)]
+    quantize_fp8_(x, flags, *out, rms_gain=rms_gain, rms_eps=rms_eps, stream=stream)
+    return tuple(out)
+
+
+def fp8_gemm(xq, s_x, wq, s_w, K: int, w_rows: bool = False, bf16: bool = False, stream=None):
+    """y [M, N] of codes and scales as quantize_fp8 gives them (w: its square form, or with `w_rows` its row form)."""
+    import torch
+
+    y = torch.empty((xq.shape[0], wq.shape[0]), dtype=torch.bfloat16 if bf16 else torch.float32, device=xq.device)
+    fp8_gemm_(xq, s_x, wq, s_w, K, (FLAG_FP8_W_ROWS if w_rows else 0) | (FLAG_BF16_OUTPUT if bf16 else 0), y, stream)
+    return y

@@ -14,6 +14,8 @@
 #include "tq.h"
 #include "tq_act.cuh"
 #include "tq_common.cuh"
+#include "tq_fp8.cuh"
+#include "tq_fp8_gemm.cuh"
 #include "tq_gemm.cuh"
 #include "tq_gemv.cuh"
 #include "tq_gemv_group.cuh"
@@ -91,6 +93,18 @@ tq_status launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t sme
                : TQ_ERR_CUDA;
 }
 
+template <typename Kern>
+tq_status set_smem_once(Kern kern, int bytes, std::atomic<int> *done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return TQ_ERR_CUDA;
+    if (!done[dev].load()) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+            return TQ_ERR_CUDA;
+        done[dev].store(1);
+    }
+    return TQ_OK;
+}
+
 // Packed-code layout from the flags (kEnc*), or -1 for the reserved value.
 inline int flag_encoding(unsigned flags) {
     const int e = (int)((flags & TQ_ENC_MASK) >> 7);
@@ -126,13 +140,13 @@ EncodeTiledFn encode_fn() {
     return f;
 }
 
-// 2-D uint8 tensor [rows][cols] (row stride = cols bytes), box [box_rows][box_cols].
+// 2-D uint8 tensor [rows][cols] (row stride ld bytes, or cols), box [box_rows][box_cols].
 bool make_tmap_u8(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, uint32_t box_cols,
-                  uint32_t box_rows, CUtensorMapSwizzle swz) {
+                  uint32_t box_rows, CUtensorMapSwizzle swz, uint64_t ld = 0) {
     EncodeTiledFn f = encode_fn();
     if (!f) return false;
     cuuint64_t dims[2] = {cols, rows};
-    cuuint64_t strides[1] = {cols};
+    cuuint64_t strides[1] = {ld ? ld : cols};
     cuuint32_t box[2] = {box_cols, box_rows};
     cuuint32_t estr[2] = {1, 1};
     return f(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
@@ -449,6 +463,78 @@ tq_status gemm_dispatch(const int8_t *xq, const float *s_x, const int32_t *rowsu
 
 
 // ---------------------------------------------------------------------------
+// Block-scaled e4m3
+// ---------------------------------------------------------------------------
+inline int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+constexpr int64_t kFp8MaxDim = 1 << 24;  // rows, columns, M, N, K
+inline int64_t fp8_blocks(int64_t v) { return (v + kFp8Block - 1) / kFp8Block; }
+
+template <bool BF16, bool VEC>
+tq_status launch_quantize_fp8(const void *x, int64_t R, int64_t C, unsigned flags, const float *gain, float eps,
+                              uint8_t *q, float *s, uint8_t *qt, float *st, cudaStream_t stream) {
+    const int64_t ldq = round_up(C, 16), ldt = round_up(R, 16);
+    const bool square = flags & TQ_FLAG_FP8_SQUARE;
+    if (flags & TQ_FLAG_RMSNORM)
+        return launch_pdl(tq_fp8_rows_norm_kernel<BF16, VEC>, dim3((unsigned)R), dim3(kActThreads), 0, stream, x, R, C,
+                          ldq, gain, eps, q, s);
+    if (!square && !qt) {
+        const int64_t segs = (C + 511) / 512;
+        return launch_pdl(tq_fp8_rows_kernel<BF16, VEC>, dim3((unsigned)((R * segs + kFp8RowWarps - 1) / kFp8RowWarps)),
+                          dim3(32 * kFp8RowWarps), 0, stream, x, R, C, ldq, segs, q, s);
+    }
+    const int64_t rb = fp8_blocks(R);
+    const dim3 grid((unsigned)fp8_blocks(C), (unsigned)(rb < 65535 ? rb : 65535));
+    if (!square)
+        return launch_pdl(tq_fp8_tile_kernel<BF16, VEC, false, true>, grid, dim3(256), 0, stream, x, R, C, ldq, ldt, q, s, qt, st);
+    if (qt)
+        return launch_pdl(tq_fp8_tile_kernel<BF16, VEC, true, true>, grid, dim3(256), 0, stream, x, R, C, ldq, ldt, q, s, qt, st);
+    return launch_pdl(tq_fp8_tile_kernel<BF16, VEC, true, false>, grid, dim3(256), 0, stream, x, R, C, ldq, ldt, q, s, qt, st);
+}
+
+template <int BT, bool ROWS>
+tq_status launch_fp8_gemm(const uint8_t *xq, const uint8_t *wq, Fp8Args a, int sms, cudaStream_t st) {
+    using L = Fp8Layout<BT>;
+    static std::atomic<int> attr_done[kMaxDevices];
+    if (tq_status e = set_smem_once(tq_fp8_gemm_kernel<BT, ROWS>, L::kDynamic, attr_done)) return e;
+    const uint64_t ld = (uint64_t)round_up(a.K, 16);
+    CUtensorMap tx, tw;
+    if (!make_tmap_u8(&tx, xq, (uint64_t)a.K, (uint64_t)a.M, kFp8Step, BT, CU_TENSOR_MAP_SWIZZLE_128B, ld) ||
+        !make_tmap_u8(&tw, wq, (uint64_t)a.K, (uint64_t)a.N, kFp8Step, kFp8TileN, CU_TENSOR_MAP_SWIZZLE_128B, ld))
+        return TQ_ERR_CUDA;
+    const int64_t tiles = ((a.M + BT - 1) / BT) * (((int64_t)a.N + kFp8TileN - 1) / kFp8TileN);
+    const int64_t blocks = fp8_blocks(a.K), slots = (int64_t)sms * L::kCtas;
+    // Few tiles: split K over the CTAs of a cluster, as far as the slots reach.
+    a.splits = 1;
+    while (a.splits < 8 && 2 * a.splits * tiles <= slots && 2 * a.splits <= blocks) a.splits *= 2;
+    const unsigned grid = (unsigned)(a.splits > 1 ? tiles * a.splits : tiles < slots ? tiles : slots);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(L::kThreads);
+    cfg.dynamicSmemBytes = L::kDynamic;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)a.splits;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, tq_fp8_gemm_kernel<BT, ROWS>, tx, tw, a) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}
+
+template <bool ROWS>
+tq_status fp8_gemm_dispatch(const uint8_t *xq, const uint8_t *wq, const Fp8Args &a, int sms, cudaStream_t st) {
+    if (a.M <= 16) return launch_fp8_gemm<16, ROWS>(xq, wq, a, sms, st);
+    if (a.M <= 32) return launch_fp8_gemm<32, ROWS>(xq, wq, a, sms, st);
+    switch (gemm_tile_tokens(a.M, a.N, sms)) {
+    case 64: return launch_fp8_gemm<64, ROWS>(xq, wq, a, sms, st);
+    case 128: return launch_fp8_gemm<128, ROWS>(xq, wq, a, sms, st);
+    default: return launch_fp8_gemm<256, ROWS>(xq, wq, a, sms, st);
+    }
+}
+
+// ---------------------------------------------------------------------------
 // Training helpers
 // ---------------------------------------------------------------------------
 // 2-D fp16 tensor [rows][cols] (row stride = 2 cols bytes), box [box_rows][box_cols].
@@ -489,18 +575,6 @@ uint64_t xs_jump(uint64_t x, int64_t n) {
     x = xs_apply(kXsWarpHost[rem / kFlipWarpRun], 1, x);
     rem %= kFlipWarpRun;
     return xs_apply(&kXsLaneHost[0][rem / kFlipRun], 32, x);
-}
-
-template <typename Kern>
-tq_status set_smem_once(Kern kern, int bytes, std::atomic<int> *done) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return TQ_ERR_CUDA;
-    if (!done[dev].load()) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-            return TQ_ERR_CUDA;
-        done[dev].store(1);
-    }
-    return TQ_OK;
 }
 
 template <bool CONV>
@@ -1149,6 +1223,65 @@ tq_status tq_bitlinear_grouped(const float *x, int64_t G, const uint8_t *const *
                               : launch_group_gemv_enc<2>(tab, pl, xq, sx, rs, y, sms, st))
         return e;
     return launch_status();
+}
+
+size_t tq_fp8_row_bytes(int64_t K) { return K > 0 ? (size_t)round_up(K, 16) : 0; }
+
+tq_status tq_quantize_fp8(const void *x, int64_t rows, int64_t cols, unsigned flags, const float *rms_gain,
+                          float rms_eps, uint8_t *q, float *s, uint8_t *qt, float *st, tq_stream_t stream) {
+    if (!x || !q || !s || (qt != nullptr) != (st != nullptr)) return TQ_ERR_NULL;
+    if (rows < 1 || cols < 1 || rows > kFp8MaxDim || cols > kFp8MaxDim) return TQ_ERR_SHAPE;
+    if (flags & ~(TQ_FLAG_BF16_INPUT | TQ_FLAG_FP8_SQUARE | TQ_FLAG_RMSNORM)) return TQ_ERR_ARG;
+    const bool rms = flags & TQ_FLAG_RMSNORM, square = flags & TQ_FLAG_FP8_SQUARE;
+    if (rms && (square || qt)) return TQ_ERR_ARG;
+    if (!rms && rms_gain) return TQ_ERR_ARG;
+    if (rms && !(rms_eps >= 0.0f && rms_eps <= 3.4028235e38f)) return TQ_ERR_ARG;
+    const void *ptrs[6] = {x, rms_gain, q, s, qt, st};
+    for (const void *p : ptrs)
+        if (p && !aligned16(p)) return TQ_ERR_ALIGN;
+    const int64_t rb = fp8_blocks(rows), cb = fp8_blocks(cols);
+    const bool bf16 = flags & TQ_FLAG_BF16_INPUT;
+    const size_t bytes[6] = {(size_t)(rows * cols) * (bf16 ? 2 : 4), (size_t)cols * 4,
+                             (size_t)(rows * round_up(cols, 16)), (size_t)(square ? rb * cb : cb * rows) * 4,
+                             (size_t)(cols * round_up(rows, 16)), (size_t)(square ? rb * cb : rb * cols) * 4};
+    for (int i = 2; i < 6; ++i)  // outputs overlap nothing
+        for (int j = 0; j < i; ++j)
+            if (ptrs[i] && ptrs[j] && overlap(ptrs[i], bytes[i], ptrs[j], bytes[j])) return TQ_ERR_ARG;
+    if (tq_status e = check_device(nullptr)) return e;
+    const bool vec = cols % 4 == 0;
+    cudaStream_t c = cs(stream);
+    if (bf16)
+        return vec ? launch_quantize_fp8<true, true>(x, rows, cols, flags, rms_gain, rms_eps, q, s, qt, st, c)
+                   : launch_quantize_fp8<true, false>(x, rows, cols, flags, rms_gain, rms_eps, q, s, qt, st, c);
+    return vec ? launch_quantize_fp8<false, true>(x, rows, cols, flags, rms_gain, rms_eps, q, s, qt, st, c)
+               : launch_quantize_fp8<false, false>(x, rows, cols, flags, rms_gain, rms_eps, q, s, qt, st, c);
+}
+
+tq_status tq_fp8_gemm(const uint8_t *xq, const float *s_x, const uint8_t *wq, const float *s_w, unsigned flags,
+                      int64_t M, int64_t N, int64_t K, void *y, tq_stream_t stream) {
+    if (!xq || !s_x || !wq || !s_w || !y) return TQ_ERR_NULL;
+    if (M < 1 || N < 1 || K < 1 || M > kFp8MaxDim || N > kFp8MaxDim || K > kFp8MaxDim) return TQ_ERR_SHAPE;
+    if (flags & ~(TQ_FLAG_FP8_W_ROWS | TQ_FLAG_BF16_OUTPUT | TQ_FLAG_ACCUMULATE | TQ_FLAG_WEIGHTS_STATIC)) return TQ_ERR_ARG;
+    const bool rows = flags & TQ_FLAG_FP8_W_ROWS, bf16 = flags & TQ_FLAG_BF16_OUTPUT;
+    if (bf16 && (flags & TQ_FLAG_ACCUMULATE)) return TQ_ERR_ARG;
+    if (!aligned16(xq) || !aligned16(s_x) || !aligned16(wq) || !aligned16(s_w) || !aligned16(y)) return TQ_ERR_ALIGN;
+    const size_t yb = (size_t)(M * N) * (bf16 ? 2 : 4), ld = (size_t)round_up(K, 16), kb = (size_t)fp8_blocks(K);
+    if (overlap(y, yb, xq, (size_t)M * ld) || overlap(y, yb, wq, (size_t)N * ld) || overlap(y, yb, s_x, kb * (size_t)M * 4) ||
+        overlap(y, yb, s_w, kb * (size_t)(rows ? N : fp8_blocks(N)) * 4))
+        return TQ_ERR_ARG;
+    int sms = 0;
+    if (tq_status e = check_device(&sms)) return e;
+    Fp8Args a{};
+    a.s_x = s_x;
+    a.s_w = s_w;
+    a.y = y;
+    a.M = (int)M;
+    a.N = (int)N;
+    a.K = (int)K;
+    a.y_bf16 = bf16 ? 1 : 0;
+    a.accumulate = (flags & TQ_FLAG_ACCUMULATE) ? 1 : 0;
+    a.w_static = (flags & TQ_FLAG_WEIGHTS_STATIC) ? 1 : 0;
+    return rows ? fp8_gemm_dispatch<true>(xq, wq, a, sms, cs(stream)) : fp8_gemm_dispatch<false>(xq, wq, a, sms, cs(stream));
 }
 
 tq_status tq_selftest_wait_timeout(uint64_t limit_ns, int sleeping, tq_stream_t stream) {
