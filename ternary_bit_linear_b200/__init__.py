@@ -350,6 +350,31 @@ def fp8_row_bytes(K: int) -> int:
     return (K + 15) // 16 * 16
 
 
+def _fit(t, dtype, shape, device, name):
+    """The check of _need for calls that last a few microseconds."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _call(fn, device, stream, *args):
+    """The C call on the tensors' device: on `stream`, or on that device's current stream."""
+    import torch
+
+    if device.type != "cuda":
+        raise ValueError(f"{fn}: expected CUDA tensors, got {device}")
+    f = getattr(_lib or load(), fn)
+    s = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+    if device.index == torch._C._cuda_getDevice():
+        code = f(*args, s)
+    else:
+        with torch.cuda.device(device):
+            code = f(*args, s)
+    if code != 0:
+        raise TqError(fn, code)
+
+
 def quantize_fp8_(x, flags, q, s, qt=None, st=None, rms_gain=None, rms_eps=1e-6, stream=None):
     """x [R, C] float32 (bfloat16 with FLAG_BF16_INPUT); q [R, fp8_row_bytes(C)]
     float8_e4m3fn; s [ceil(C/128), R], or [ceil(R/128), ceil(C/128)] with
@@ -358,17 +383,14 @@ def quantize_fp8_(x, flags, q, s, qt=None, st=None, rms_gain=None, rms_eps=1e-6,
 
     R, C = x.shape
     rb, cb = -(-R // 128), -(-C // 128)
-    square = bool(flags & FLAG_FP8_SQUARE)
-    f8 = torch.float8_e4m3fn
-    _need(x, torch.bfloat16 if flags & FLAG_BF16_INPUT else torch.float32, (R, C), "x")
-    _need(q, f8, (R, fp8_row_bytes(C)), "q")
-    _need(s, torch.float32, (rb, cb) if square else (cb, R), "s")
-    _need(qt, f8, (C, fp8_row_bytes(R)), "qt")
-    _need(st, torch.float32, (cb, rb) if square else (rb, C), "st")
-    _need(rms_gain, torch.float32, (C,), "rms_gain")
-    _check("tq_quantize_fp8",
-           load().tq_quantize_fp8(_ptr(x), R, C, flags, _ptr(rms_gain), float(rms_eps), _ptr(q), _ptr(s), _ptr(qt),
-                                  _ptr(st), _stream(stream)))
+    square, dev, f8, f32 = flags & FLAG_FP8_SQUARE, x.device, torch.float8_e4m3fn, torch.float32
+    _call("tq_quantize_fp8", dev, stream,
+          _fit(x, torch.bfloat16 if flags & FLAG_BF16_INPUT else f32, (R, C), dev, "x"), R, C, flags,
+          None if rms_gain is None else _fit(rms_gain, f32, (C,), dev, "rms_gain"), rms_eps,
+          _fit(q, f8, (R, (C + 15) // 16 * 16), dev, "q"),
+          _fit(s, f32, (rb, cb) if square else (cb, R), dev, "s"),
+          None if qt is None else _fit(qt, f8, (C, (R + 15) // 16 * 16), dev, "qt"),
+          None if st is None else _fit(st, f32, (cb, rb) if square else (rb, C), dev, "st"))
 
 
 def fp8_gemm_(xq, s_x, wq, s_w, K, flags, y, stream=None):
@@ -377,15 +399,12 @@ def fp8_gemm_(xq, s_x, wq, s_w, K, flags, y, stream=None):
     FLAG_FP8_W_ROWS; y [M, N] float32, or bfloat16 with FLAG_BF16_OUTPUT."""
     import torch
 
-    M, N, ld, kb = xq.shape[0], wq.shape[0], fp8_row_bytes(K), -(-K // 128)
-    f8 = torch.float8_e4m3fn
-    _need(xq, f8, (M, ld), "xq")
-    _need(wq, f8, (N, ld), "wq")
-    _need(s_x, torch.float32, (kb, M), "s_x")
-    _need(s_w, torch.float32, (kb, N) if flags & FLAG_FP8_W_ROWS else (-(-N // 128), kb), "s_w")
-    _need(y, torch.bfloat16 if flags & FLAG_BF16_OUTPUT else torch.float32, (M, N), "y")
-    _check("tq_fp8_gemm",
-           load().tq_fp8_gemm(_ptr(xq), _ptr(s_x), _ptr(wq), _ptr(s_w), flags, M, N, K, _ptr(y), _stream(stream)))
+    M, N, ld, kb = xq.shape[0], wq.shape[0], (K + 15) // 16 * 16, -(-K // 128)
+    dev, f8, f32 = xq.device, torch.float8_e4m3fn, torch.float32
+    _call("tq_fp8_gemm", dev, stream, _fit(xq, f8, (M, ld), dev, "xq"), _fit(s_x, f32, (kb, M), dev, "s_x"),
+          _fit(wq, f8, (N, ld), dev, "wq"),
+          _fit(s_w, f32, (kb, N) if flags & FLAG_FP8_W_ROWS else (-(-N // 128), kb), dev, "s_w"), flags, M, N, K,
+          _fit(y, torch.bfloat16 if flags & FLAG_BF16_OUTPUT else f32, (M, N), dev, "y"))
 
 
 def backward_input_workspace_bytes(M: int, N: int) -> int:
@@ -530,19 +549,21 @@ def quantize_fp8(x, square: bool = False, transpose: bool = False, rmsnorm: bool
     R, C = x.shape
     rb, cb = -(-R // 128), -(-C // 128)
     flags = ((FLAG_FP8_SQUARE if square else 0) | (FLAG_RMSNORM if rmsnorm else 0) |
-             (FLAG_BF16_INPUT if x.dtype == torch.bfloat16 else 0))
-    new = lambda shape, dt: torch.empty(shape, dtype=dt, device=x.device)  # noqa: E731
-    out = [new((R, fp8_row_bytes(C)), torch.float8_e4m3fn), new((rb, cb) if square else (cb, R), torch.float32)]
-    if transpose:
-        out += [new((C, fp8_row_bytes(R)), torch.float8_e4m3fn), new((cb, rb) if square else (rb, C), torch.float32)]
-    quantize_fp8_(x, flags, *out, rms_gain=rms_gain, rms_eps=rms_eps, stream=stream)
-    return tuple(out)
+             (FLAG_BF16_INPUT if x.dtype is torch.bfloat16 else 0))
+    f8, f32 = torch.float8_e4m3fn, torch.float32
+    q, s = x.new_empty((R, fp8_row_bytes(C)), dtype=f8), x.new_empty((rb, cb) if square else (cb, R), dtype=f32)
+    if not transpose:
+        quantize_fp8_(x, flags, q, s, None, None, rms_gain, rms_eps, stream)
+        return q, s
+    qt, st = x.new_empty((C, fp8_row_bytes(R)), dtype=f8), x.new_empty((cb, rb) if square else (rb, C), dtype=f32)
+    quantize_fp8_(x, flags, q, s, qt, st, rms_gain, rms_eps, stream)
+    return q, s, qt, st
 
 
 def fp8_gemm(xq, s_x, wq, s_w, K: int, w_rows: bool = False, bf16: bool = False, stream=None):
     """y [M, N] of codes and scales as quantize_fp8 gives them (w: its square form, or with `w_rows` its row form)."""
     import torch
 
-    y = torch.empty((xq.shape[0], wq.shape[0]), dtype=torch.bfloat16 if bf16 else torch.float32, device=xq.device)
+    y = xq.new_empty((xq.shape[0], wq.shape[0]), dtype=torch.bfloat16 if bf16 else torch.float32)
     fp8_gemm_(xq, s_x, wq, s_w, K, (FLAG_FP8_W_ROWS if w_rows else 0) | (FLAG_BF16_OUTPUT if bf16 else 0), y, stream)
     return y

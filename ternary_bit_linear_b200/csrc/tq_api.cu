@@ -491,6 +491,13 @@ tq_status launch_quantize_fp8(const void *x, int64_t R, int64_t C, unsigned flag
     return launch_pdl(tq_fp8_tile_kernel<BF16, VEC, true, false>, grid, dim3(256), 0, stream, x, R, C, ldq, ldt, q, s, qt, st);
 }
 
+// Few tiles: K is split over the CTAs of a cluster, as far as the slots reach.
+inline int64_t fp8_splits(int64_t tiles, int64_t blocks, int64_t slots) {
+    int64_t s = 1;
+    while (s < 8 && 2 * s * tiles <= slots && 2 * s <= blocks) s *= 2;
+    return s;
+}
+
 template <int BT, bool ROWS>
 tq_status launch_fp8_gemm(const uint8_t *xq, const uint8_t *wq, Fp8Args a, int sms, cudaStream_t st) {
     using L = Fp8Layout<BT>;
@@ -503,9 +510,7 @@ tq_status launch_fp8_gemm(const uint8_t *xq, const uint8_t *wq, Fp8Args a, int s
         return TQ_ERR_CUDA;
     const int64_t tiles = ((a.M + BT - 1) / BT) * (((int64_t)a.N + kFp8TileN - 1) / kFp8TileN);
     const int64_t blocks = fp8_blocks(a.K), slots = (int64_t)sms * L::kCtas;
-    // Few tiles: split K over the CTAs of a cluster, as far as the slots reach.
-    a.splits = 1;
-    while (a.splits < 8 && 2 * a.splits * tiles <= slots && 2 * a.splits <= blocks) a.splits *= 2;
+    a.splits = (int)fp8_splits(tiles, blocks, slots);
     const unsigned grid = (unsigned)(a.splits > 1 ? tiles * a.splits : tiles < slots ? tiles : slots);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
@@ -523,15 +528,56 @@ tq_status launch_fp8_gemm(const uint8_t *xq, const uint8_t *wq, Fp8Args a, int s
     return cudaLaunchKernelEx(&cfg, tq_fp8_gemm_kernel<BT, ROWS>, tx, tw, a) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
+template <int BN>
+tq_status launch_fp8_gemm_wide(const uint8_t *xq, const uint8_t *wq, Fp8Args a, int sms, cudaStream_t st) {
+    using L = Fp8WideLayout<BN>;
+    static std::atomic<int> attr_done[kMaxDevices];
+    if (tq_status e = set_smem_once(tq_fp8_gemm_wide_kernel<BN>, L::kDynamic, attr_done)) return e;
+    const uint64_t ld = (uint64_t)round_up(a.K, 16);
+    CUtensorMap tx, tw;
+    if (!make_tmap_u8(&tx, xq, (uint64_t)a.K, (uint64_t)a.M, kFp8Step, 128, CU_TENSOR_MAP_SWIZZLE_128B, ld) ||
+        !make_tmap_u8(&tw, wq, (uint64_t)a.K, (uint64_t)a.N, kFp8Step, BN, CU_TENSOR_MAP_SWIZZLE_128B, ld))
+        return TQ_ERR_CUDA;
+    const int64_t tiles = (((int64_t)a.M + 127) / 128) * (((int64_t)a.N + BN - 1) / BN);
+    const unsigned grid = (unsigned)(tiles < sms ? tiles : sms);
+    return launch_pdl(tq_fp8_gemm_wide_kernel<BN>, dim3(grid), dim3(L::kThreads), L::kDynamic, st, tx, tw, a);
+}
+
+// Up to 32 tokens: the smallest tile that holds them (the bytes of w bound the
+// call).  More: the variant whose rounds of tiles take least, at the measured
+// time of one block of K in one tile (2048 x 11008 x 4096 and single waves of
+// 4096 x 4096 with each): 0.55 us for 64 and 0.62 us for 128 tokens (narrow, K
+// split while SMs are idle), 0.46 us for 128 tokens x 128 rows of w and 0.74 us
+// for 128 x 256 (wide).  Filling the pipeline and storing take about eight
+// blocks' time, and joining a split as long again (333 x 1000 x 1410: 12.2 us
+// with 64 tokens and two parts, 8.3 us wide; 128 x 4096 x 4096: 12.2 us with 128
+// tokens and four parts, 15.8 us wide).  Scales per row of w only in the narrow
+// kernel.
 template <bool ROWS>
 tq_status fp8_gemm_dispatch(const uint8_t *xq, const uint8_t *wq, const Fp8Args &a, int sms, cudaStream_t st) {
     if (a.M <= 16) return launch_fp8_gemm<16, ROWS>(xq, wq, a, sms, st);
     if (a.M <= 32) return launch_fp8_gemm<32, ROWS>(xq, wq, a, sms, st);
-    switch (gemm_tile_tokens(a.M, a.N, sms)) {
-    case 64: return launch_fp8_gemm<64, ROWS>(xq, wq, a, sms, st);
-    case 128: return launch_fp8_gemm<128, ROWS>(xq, wq, a, sms, st);
-    default: return launch_fp8_gemm<256, ROWS>(xq, wq, a, sms, st);
+    const int64_t blocks = fp8_blocks(a.K);
+    int best = 0;
+    double best_us = 0.0;
+    const struct {
+        int m, n, wide;
+        double us;
+    } kinds[4] = {{64, 128, 0, 0.55}, {128, 128, 0, 0.62}, {128, 128, 1, 0.46}, {128, 256, 1, 0.74}};
+    for (int i = 0; i < (ROWS ? 2 : 4); ++i) {
+        const int64_t tiles = ((a.M + kinds[i].m - 1) / kinds[i].m) * (((int64_t)a.N + kinds[i].n - 1) / kinds[i].n);
+        const int64_t split = kinds[i].wide ? 1 : fp8_splits(tiles, blocks, sms);
+        const double us = kinds[i].us * (double)((tiles * split + sms - 1) / sms * ((blocks + split - 1) / split) + (split > 1 ? 16 : 8));
+        if (i == 0 || us < best_us) {
+            best = i;
+            best_us = us;
+        }
     }
+    if constexpr (!ROWS) {
+        if (best == 2) return launch_fp8_gemm_wide<128>(xq, wq, a, sms, st);
+        if (best == 3) return launch_fp8_gemm_wide<256>(xq, wq, a, sms, st);
+    }
+    return best == 0 ? launch_fp8_gemm<64, ROWS>(xq, wq, a, sms, st) : launch_fp8_gemm<128, ROWS>(xq, wq, a, sms, st);
 }
 
 // ---------------------------------------------------------------------------
