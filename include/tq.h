@@ -369,6 +369,55 @@ TQ_API tq_status tq_swiglu_mlp(const float *x, int64_t M, int64_t d_model, int64
 TQ_API size_t tq_swiglu_workspace_bytes(int64_t M, int64_t d_model, int64_t d_ffn, unsigned flags);
 
 /*
+ * A whole mixture-of-experts feed-forward layer for the few tokens of a decode
+ * step: router, choice of experts, the chosen experts' clamped SwiGLU blocks
+ * (tq_swiglu_mlp's, each three ternary layers) and their weighted sum, in two
+ * launches.
+ *
+ *   l[m][e]   = fp32(sum_d x[m][d] * router[e][d])          (summed in fp64)
+ *   ids[m]    = the top_k experts of the largest l[m][e], largest first, ties to
+ *               the lower index (a NaN ranks below every number)
+ *   w[m][j]   = exp(l[m][ids_j] - max l) / sum_e exp(l[m][e] - max l); with
+ *               TQ_FLAG_NORM_TOPK the sum runs over the chosen experts only
+ *   y[m]      = sum_j w[m][j] * expert_{ids_j}(x[m]), slots in order
+ *
+ * Every expert quantises the same rotated (and with TQ_FLAG_RMSNORM normalised)
+ * token; SiLU(gate) * up is evaluated in fp64 and rounded to fp32 before the
+ * clamp and the down projection's own [RMSNorm,] rotation and quantisation.
+ *
+ *   x          [M][d_model] fp32.  1 <= M <= 64; d_model, d_ffn multiples of 512,
+ *              at most 8192; 1 <= n_experts <= 256; top_k <= 16, n_experts.  For
+ *              more tokens, tq_swiglu_mlp per expert.
+ *   router     [n_experts][d_model] fp32, or NULL: expert_ids and expert_weights
+ *              are then inputs.  An id outside [0, n_experts) marks an unused slot (a
+ *              padded token, an expert of another rank): it adds nothing, and a
+ *              token without used slots gives y = 0.  An id may occur twice.
+ *   gate_*, up_*, down_*   the experts' layers one after another: packed
+ *              [n_experts][d_ffn][d_model/4] (down: [n_experts][d_model][d_ffn/4]) in
+ *              the layout the flags name; gamma [n_experts], or [n_experts][rows]
+ *              with TQ_GAMMA_PER_ROW.
+ *   y          [M][d_model] fp32, written.
+ *   expert_ids, expert_weights   [M][top_k] int32 and fp32: written if there is a
+ *              router, else read.
+ *   workspace  tq_moe_workspace_bytes(...) bytes (0 for shapes that the call
+ *              refuses); contents on entry are ignored.  Calls that may run at the
+ *              same time need their own.
+ *   flags      TQ_FLAG_FWHT (required), TQ_FLAG_RMSNORM, TQ_FLAG_NORM_TOPK (with a
+ *              router only), TQ_GAMMA_PER_ROW, TQ_FLAG_SANITIZE_NONFINITE (of x, for
+ *              the router too, and of the activations), TQ_FLAG_WEIGHTS_STATIC, TQ_ENC_*.
+ * The second launch is a cooperative one, one block per SM whose blocks wait for
+ * one another (each wait bounded): it starts when the whole GPU has room for it.
+ */
+TQ_API tq_status tq_moe_swiglu(const float *x, int64_t M, int64_t d_model, int64_t d_ffn, int64_t n_experts,
+                               int64_t top_k, unsigned flags, float clamp_val, const float *router,
+                               const uint8_t *gate_packed, const float *gate_gamma, const uint8_t *up_packed,
+                               const float *up_gamma, const uint8_t *down_packed, const float *down_gamma, float *y,
+                               int32_t *expert_ids, float *expert_weights, void *workspace, size_t workspace_bytes,
+                               tq_stream_t stream);
+TQ_API size_t tq_moe_workspace_bytes(int64_t M, int64_t d_model, int64_t d_ffn, int64_t n_experts, int64_t top_k,
+                                     unsigned flags);
+
+/*
  * Quantisation to 8-bit floating point (e4m3) with one fp32 scale per block of
  * 128, for the layers that a network keeps out of ternary (tq_fp8_gemm):
  *

@@ -61,6 +61,9 @@ SIGNATURES = {
     "tq_swiglu_workspace_bytes": (_SZ, [_I64, _I64, _I64, _U]),
     "tq_bitlinear_grouped": (_I, [_P, _I64, _P, _P, _U, _I64, _I64, _I64, _P, _P, _SZ, _P]),
     "tq_grouped_workspace_bytes": (_SZ, [_I64, _I64, _I64, _U]),
+    "tq_moe_swiglu": (_I, [_P, _I64, _I64, _I64, _I64, _I64, _U, _F, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ,
+                           _P]),
+    "tq_moe_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64, _U]),
     "tq_quantize_fp8": (_I, [_P, _I64, _I64, _U, _P, _F, _P, _P, _P, _P, _P]),
     "tq_fp8_row_bytes": (_SZ, [_I64]),
     "tq_fp8_gemm": (_I, [_P, _P, _P, _P, _U, _I64, _I64, _I64, _P, _P]),
@@ -375,6 +378,31 @@ def _call(fn, device, stream, *args):
         raise TqError(fn, code)
 
 
+def moe_workspace_bytes(M: int, d_model: int, d_ffn: int, n_experts: int, top_k: int, flags: int) -> int:
+    return load().tq_moe_workspace_bytes(M, d_model, d_ffn, n_experts, top_k, flags)
+
+
+def moe_swiglu_(x, router, gate, up, down, flags, y, ids, weights, workspace, clamp_val=10.0, stream=None):
+    """gate, up, down: (packed, gamma) pairs, the experts stacked along the first
+    dimension; router [E, D] float32, or None: ids [M, k] int32 and weights [M, k]
+    float32 are then read (an id outside [0, E): no expert) instead of written."""
+    import torch
+
+    M, D = x.shape
+    E, F = gate[0].shape[0], gate[0].shape[1]
+    k = ids.shape[1]
+    dev, f32, u8 = x.device, torch.float32, torch.uint8
+    gf, gd = ((E, F), (E, D)) if flags & GAMMA_PER_ROW else ((E,), (E,))
+    _call("tq_moe_swiglu", dev, stream, _fit(x, f32, (M, D), dev, "x"), M, D, F, E, k, flags, clamp_val,
+          None if router is None else _fit(router, f32, (E, D), dev, "router"),
+          _fit(gate[0], u8, (E, F, D // 4), dev, "gate packed"), _fit(gate[1], f32, gf, dev, "gate gamma"),
+          _fit(up[0], u8, (E, F, D // 4), dev, "up packed"), _fit(up[1], f32, gf, dev, "up gamma"),
+          _fit(down[0], u8, (E, D, F // 4), dev, "down packed"), _fit(down[1], f32, gd, dev, "down gamma"),
+          _fit(y, f32, (M, D), dev, "y"), _fit(ids, torch.int32, (M, k), dev, "ids"),
+          _fit(weights, f32, (M, k), dev, "weights"), workspace.data_ptr(),
+          workspace.numel() * workspace.element_size())
+
+
 def quantize_fp8_(x, flags, q, s, qt=None, st=None, rms_gain=None, rms_eps=1e-6, stream=None):
     """x [R, C] float32 (bfloat16 with FLAG_BF16_INPUT); q [R, fp8_row_bytes(C)]
     float8_e4m3fn; s [ceil(C/128), R], or [ceil(R/128), ceil(C/128)] with
@@ -539,6 +567,23 @@ def bitlinear_fused(x, packed, gamma, per_row: bool, rmsnorm: bool = True, fwht:
     bitlinear_fused_(x, packed, gamma, flags, y, ws, rms_gain, rms_eps, eta_min, eta_max, xq, sx,
                      stream)
     return (y, xq, sx) if return_xq else y
+
+
+def moe_swiglu(x, router, gate, up, down, top_k: int, per_row: bool = False, rmsnorm: bool = True,
+               norm_topk: bool = True, sanitize: bool = False, clamp_val: float = 10.0, stream=None):
+    """A mixture-of-experts layer for up to 64 tokens: (y, ids, weights)."""
+    import torch
+
+    M, D = x.shape
+    E, F = gate[0].shape[0], gate[0].shape[1]
+    flags = (FLAG_FWHT | (GAMMA_PER_ROW if per_row else 0) | (FLAG_RMSNORM if rmsnorm else 0) |
+             (FLAG_NORM_TOPK if norm_topk else 0) | (FLAG_SANITIZE_NONFINITE if sanitize else 0))
+    y = torch.empty_like(x)
+    ids = x.new_empty((M, top_k), dtype=torch.int32)
+    weights = x.new_empty((M, top_k))
+    ws = x.new_empty((moe_workspace_bytes(M, D, F, E, top_k, flags),), dtype=torch.uint8)
+    moe_swiglu_(x, router, gate, up, down, flags, y, ids, weights, ws, clamp_val, stream)
+    return y, ids, weights
 
 
 def quantize_fp8(x, square: bool = False, transpose: bool = False, rmsnorm: bool = False, rms_gain=None,

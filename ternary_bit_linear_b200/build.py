@@ -19,7 +19,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libtq.so")
 SOURCES = ["tq_api.cu"]
 DEPS = ["tq_api.cu", "tq_common.cuh", "tq_pack.cuh", "tq_act.cuh", "tq_gemv.cuh", "tq_gemv_group.cuh", "tq_gemm.cuh",
-        "tq_fp8.cuh", "tq_fp8_gemm.cuh", "tq_train.cuh", "tq_xorshift_jump.h"]
+        "tq_moe.cuh", "tq_fp8.cuh", "tq_fp8_gemm.cuh", "tq_train.cuh", "tq_xorshift_jump.h"]
 
 
 def nvcc() -> str:

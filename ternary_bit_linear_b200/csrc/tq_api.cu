@@ -19,6 +19,7 @@
 #include "tq_gemm.cuh"
 #include "tq_gemv.cuh"
 #include "tq_gemv_group.cuh"
+#include "tq_moe.cuh"
 #include "tq_pack.cuh"
 #include "tq_train.cuh"
 
@@ -578,6 +579,46 @@ tq_status fp8_gemm_dispatch(const uint8_t *xq, const uint8_t *wq, const Fp8Args 
         if (best == 3) return launch_fp8_gemm_wide<256>(xq, wq, a, sms, st);
     }
     return best == 0 ? launch_fp8_gemm<64, ROWS>(xq, wq, a, sms, st) : launch_fp8_gemm<128, ROWS>(xq, wq, a, sms, st);
+}
+
+// ---------------------------------------------------------------------------
+// Mixture of experts
+// ---------------------------------------------------------------------------
+// Byte offsets of the workspace's parts: barrier, x_q, s_x, rowsum, logits, then
+// per (token, slot): activations, their codes, scales and rowsums, outputs.
+size_t moe_parts(int64_t M, int64_t D, int64_t F, int64_t E, int64_t k, size_t (&off)[10]) {
+    const int64_t P = M * k;
+    const size_t bytes[10] = {256, (size_t)(M * D), (size_t)M * 4, (size_t)M * 4, (size_t)(M * E) * 4,
+                              (size_t)(P * F) * 4, (size_t)(P * F), (size_t)P * 4, (size_t)P * 4, (size_t)(P * D) * 4};
+    size_t at = 0;
+    for (int i = 0; i < 10; ++i) {
+        off[i] = at;
+        at += (bytes[i] + 255) & ~(size_t)255;
+    }
+    return at;
+}
+
+inline bool moe_shape_ok(int64_t M, int64_t D, int64_t F, int64_t E, int64_t k) {
+    return M >= 1 && M <= kMoeMaxTokens && D >= 512 && D <= kMoeMaxK && D % 512 == 0 && F >= 512 && F <= kMoeMaxK &&
+           F % 512 == 0 && E >= 1 && E <= kMoeMaxExperts && k >= 1 && k <= kMoeMaxTopk && k <= E;
+}
+
+template <bool CONV>
+tq_status launch_moe_experts(const MoeArgs &a, int sms, cudaStream_t st) {
+    static std::atomic<int> attr_done[kMaxDevices];
+    constexpr int kMost = kMoeRedBytes + kMoeChunk * (kMoeMaxK + 128);
+    if (tq_status e = set_smem_once(tq_moe_experts_kernel<CONV>, kMost, attr_done)) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)sms);
+    cfg.blockDim = dim3(kMoeThreads);
+    cfg.dynamicSmemBytes = (size_t)(kMoeRedBytes + kMoeChunk * gemv_x_stride(a.D > a.F ? a.D : a.F));
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;  // its CTAs wait for one another
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tq_moe_experts_kernel<CONV>, a) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------------------
@@ -1328,6 +1369,88 @@ tq_status tq_fp8_gemm(const uint8_t *xq, const float *s_x, const uint8_t *wq, co
     a.accumulate = (flags & TQ_FLAG_ACCUMULATE) ? 1 : 0;
     a.w_static = (flags & TQ_FLAG_WEIGHTS_STATIC) ? 1 : 0;
     return rows ? fp8_gemm_dispatch<true>(xq, wq, a, sms, cs(stream)) : fp8_gemm_dispatch<false>(xq, wq, a, sms, cs(stream));
+}
+
+size_t tq_moe_workspace_bytes(int64_t M, int64_t d_model, int64_t d_ffn, int64_t n_experts, int64_t top_k,
+                              unsigned flags) {
+    (void)flags;
+    if (!moe_shape_ok(M, d_model, d_ffn, n_experts, top_k)) return 0;
+    size_t off[10];
+    return moe_parts(M, d_model, d_ffn, n_experts, top_k, off);
+}
+
+tq_status tq_moe_swiglu(const float *x, int64_t M, int64_t d_model, int64_t d_ffn, int64_t n_experts, int64_t top_k,
+                        unsigned flags, float clamp_val, const float *router, const uint8_t *gate_packed,
+                        const float *gate_gamma, const uint8_t *up_packed, const float *up_gamma,
+                        const uint8_t *down_packed, const float *down_gamma, float *y, int32_t *expert_ids,
+                        float *expert_weights, void *workspace, size_t workspace_bytes, tq_stream_t stream) {
+    if (!x || !gate_packed || !gate_gamma || !up_packed || !up_gamma || !down_packed || !down_gamma || !y ||
+        !expert_ids || !expert_weights || !workspace)
+        return TQ_ERR_NULL;
+    if (!moe_shape_ok(M, d_model, d_ffn, n_experts, top_k)) return TQ_ERR_SHAPE;
+    const unsigned known = TQ_GAMMA_PER_ROW | TQ_FLAG_FWHT | TQ_FLAG_RMSNORM | TQ_FLAG_SANITIZE_NONFINITE |
+                           TQ_FLAG_WEIGHTS_STATIC | TQ_FLAG_NORM_TOPK | TQ_ENC_MASK;
+    const int enc = flag_encoding(flags);
+    if ((flags & ~known) || !(flags & TQ_FLAG_FWHT) || enc < 0 || ((flags & TQ_FLAG_NORM_TOPK) && !router)) return TQ_ERR_ARG;
+    if (!(clamp_val > 0.0f && clamp_val < 3.0e38f)) return TQ_ERR_ARG;
+    size_t off[10];
+    const size_t need = moe_parts(M, d_model, d_ffn, n_experts, top_k, off);
+    const size_t xb = (size_t)(M * d_model) * 4, pb = (size_t)(n_experts * d_ffn * d_model / 4), kb = (size_t)(M * top_k) * 4;
+    const bool pr = flags & TQ_GAMMA_PER_ROW;
+    const size_t gb = (size_t)n_experts * (pr ? (size_t)d_ffn : 1) * 4, db = (size_t)n_experts * (pr ? (size_t)d_model : 1) * 4;
+    // inputs, then what is written; ids and weights are inputs when there is no router
+    const void *ptr[12] = {x, router, gate_packed, gate_gamma, up_packed, up_gamma, down_packed, down_gamma,
+                           expert_ids, expert_weights, y, workspace};
+    const size_t bytes[12] = {xb, (size_t)(n_experts * d_model) * 4, pb, gb, pb, gb, pb, db, kb, kb, xb, need};
+    for (const void *p : ptr)
+        if (p && !aligned16(p)) return TQ_ERR_ALIGN;
+    if (workspace_bytes < need) return TQ_ERR_ARG;
+    for (int i = 8; i < 12; ++i)
+        for (int j = 0; j < i; ++j)
+            if (ptr[j] && overlap(ptr[i], bytes[i], ptr[j], bytes[j])) return TQ_ERR_ARG;
+    int sms = 0;
+    if (tq_status e = check_device(&sms)) return e;
+    uint8_t *ws = reinterpret_cast<uint8_t *>(workspace);
+    MoeArgs a{};
+    a.x = x;
+    a.router = router;
+    a.gate = gate_packed;
+    a.up = up_packed;
+    a.down = down_packed;
+    a.gate_gamma = gate_gamma;
+    a.up_gamma = up_gamma;
+    a.down_gamma = down_gamma;
+    a.y = y;
+    a.ids = expert_ids;
+    a.weights = expert_weights;
+    a.M = (int)M;
+    a.D = (int)d_model;
+    a.F = (int)d_ffn;
+    a.E = (int)n_experts;
+    a.k = (int)top_k;
+    a.per_row = pr ? 1 : 0;
+    a.norm_topk = (flags & TQ_FLAG_NORM_TOPK) ? 1 : 0;
+    a.enc = enc;
+    a.clamp_val = clamp_val;
+    a.act.sanitize = (flags & TQ_FLAG_SANITIZE_NONFINITE) ? 1 : 0;
+    a.act.eta_max = 40.0f;  // as in tq_swiglu_mlp
+    a.act.eta_min = 0.05f;
+    a.act.rmsnorm = (flags & TQ_FLAG_RMSNORM) ? 1 : 0;
+    a.act.rms_eps = 1e-6f;
+    a.barrier = reinterpret_cast<unsigned *>(ws + off[0]);
+    a.xq = reinterpret_cast<int8_t *>(ws + off[1]);
+    a.sx = reinterpret_cast<float *>(ws + off[2]);
+    a.rs = reinterpret_cast<int32_t *>(ws + off[3]);
+    a.logits = reinterpret_cast<float *>(ws + off[4]);
+    a.h = reinterpret_cast<float *>(ws + off[5]);
+    a.hq = reinterpret_cast<int8_t *>(ws + off[6]);
+    a.sh = reinterpret_cast<float *>(ws + off[7]);
+    a.rh = reinterpret_cast<int32_t *>(ws + off[8]);
+    a.out = reinterpret_cast<float *>(ws + off[9]);
+    cudaStream_t st = cs(stream);
+    const int64_t units = router ? (n_experts + kMoeWarps - 1) / kMoeWarps * ((M + kMoeRouteTokens - 1) / kMoeRouteTokens) : 0;
+    if (tq_status e = launch_pdl(tq_moe_route_kernel, dim3((unsigned)(M + units)), dim3(kMoeThreads), 0, st, a)) return e;
+    return enc != kEncFoundry ? launch_moe_experts<true>(a, sms, st) : launch_moe_experts<false>(a, sms, st);
 }
 
 tq_status tq_selftest_wait_timeout(uint64_t limit_ns, int sleeping, tq_stream_t stream) {
