@@ -18,12 +18,12 @@
 // bytes each); for one or two tokens, the chain of dependent steps.
 //
 //   tq_moe_route_kernel: a CTA per token quantises it; the other CTAs compute the
-//     logits, a warp per expert and four tokens.
+//     logits of 16 experts and four tokens each.
 //   tq_moe_experts_kernel: one CTA per SM, launched cooperatively (all CTAs
 //     resident), with three grid-wide barriers between its phases:
 //       choice     every CTA picks every token's experts (cheaper than another
 //                  barrier) and sorts the (token, slot) pairs by expert; an expert
-//                  and up to 16 of its pairs are one "problem".
+//                  and up to 8 of its pairs are one "problem".
 //       gate, up   a strip is 16 rows of both matrices, so that the activation
 //                  follows in registers.  The strips of all problems are split
 //                  into contiguous runs, one per CTA; the quantised tokens of a
@@ -32,10 +32,10 @@
 //       down       strips of 32 rows, runs as before.
 //       sum        y from the pairs' outputs, slots in order: no atomics, and
 //                  the result does not depend on how pairs were grouped.
-//   A warp streams its strips' weights from HBM into registers, several 64-byte
-//   column steps ahead, and contracts them with mma.sync (u8 codes x s8): with at
-//   most 16 tokens the tensor rate is no bound, and no shared memory is spent on
-//   bytes that are used once.
+//   A warp streams its strips' weights from HBM into registers, two column steps
+//   (4 KB) ahead and across strips, and contracts them with mma.sync (u8 codes x
+//   s8): for 8 tokens the tensor rate is no bound, and no shared memory is spent
+//   on bytes that are used once.
 #pragma once
 
 #include "tq_act.cuh"
@@ -48,12 +48,13 @@ constexpr int kMoeWarps = 16;
 constexpr int kMoeThreads = 32 * kMoeWarps;
 constexpr int kMoeMaxTokens = 64, kMoeMaxTopk = 16, kMoeMaxExperts = 256;
 constexpr int kMoeMaxPairs = kMoeMaxTokens * kMoeMaxTopk;
-constexpr int kMoeChunk = 16;  // pairs of one expert per problem
+constexpr int kMoeChunk = 8;  // pairs of one expert per problem: the MMA's 8 columns
 constexpr int kMoeMaxProblems = kMoeMaxExperts + kMoeMaxPairs / kMoeChunk;
 constexpr int kMoeMaxK = 8192;  // d_model, d_ffn: 16 blocks of 512, one per warp
 constexpr int kMoeRouteTokens = 4;
-// partial sums of a split strip: [2][warps][2 matrices x 2 token blocks x 4][lanes]
-constexpr int kMoeRedBytes = 2 * kMoeWarps * 16 * 32 * 4;
+constexpr int kMoeSlot = 8 * 32;  // 32-bit words of a warp's exchange slot
+constexpr int kMoeRedBytes = 2 * kMoeWarps * kMoeSlot * 4;
+static_assert(kMoeRedBytes >= kMoeMaxPairs / 32 * kMoeMaxExperts * 2, "the pair counts fit the exchange slots");
 
 struct MoeArgs {
     const float *x, *router;  // [M][D], [E][D] or nullptr (ids, weights given)
@@ -166,10 +167,13 @@ __device__ __forceinline__ void load_block16(float (&f)[16], const float *row, i
     }
 }
 
-// CTAs 0 .. M - 1: token blockIdx.x's codes.  The others: logits of 16 experts
-// (a warp each) and 4 tokens.
+// CTAs 0 .. M - 1: token blockIdx.x's codes.  The others: logits of 16 experts and
+// 4 tokens, a warp for 4 experts and a quarter of d_model (so that a converted
+// value enters four products, and few tokens still spread over many lanes); the
+// quarters are added in order.
 __global__ void __launch_bounds__(kMoeThreads) tq_moe_route_kernel(const __grid_constant__ MoeArgs a) {
     __shared__ MoeRed red;
+    __shared__ double part[kMoeWarps][4 * kMoeRouteTokens];
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -183,39 +187,55 @@ __global__ void __launch_bounds__(kMoeThreads) tq_moe_route_kernel(const __grid_
         return;
     }
     const int u = blockIdx.x - a.M, tgroups = (a.M + kMoeRouteTokens - 1) / kMoeRouteTokens;
-    const int e = u / tgroups * kMoeWarps + warp, m0 = u % tgroups * kMoeRouteTokens;
-    if (e >= a.E) return;
+    const int e0 = u / tgroups * kMoeWarps + (warp >> 2) * 4, m0 = u % tgroups * kMoeRouteTokens;
     const int nt = a.M - m0 < kMoeRouteTokens ? a.M - m0 : kMoeRouteTokens;
-    const float4 *wr = reinterpret_cast<const float4 *>(a.router + (int64_t)e * a.D);
-    const float4 *xr = reinterpret_cast<const float4 *>(a.x + (int64_t)m0 * a.D);
-    const int nv = a.D / 4;  // a multiple of 128
-    double s[kMoeRouteTokens] = {0.0, 0.0, 0.0, 0.0};
-    for (int i = lane; i < nv; i += 128) {
-        float4 w[4];
+    const int nv = a.D / 4, q0 = (warp & 3) * (nv / 4);  // float4; a quarter is a multiple of 32
+    const float4 *wr[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = __ldg(wr + i + 32 * j);
+    for (int i = 0; i < 4; ++i)  // experts past the last: the last again, not stored
+        wr[i] = reinterpret_cast<const float4 *>(a.router + (int64_t)(e0 + i < a.E ? e0 + i : a.E - 1) * a.D) + q0 + lane;
+    const float4 *xr = reinterpret_cast<const float4 *>(a.x + (int64_t)m0 * a.D) + q0 + lane;
+    double s[4][kMoeRouteTokens];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int t = 0; t < kMoeRouteTokens; ++t) s[i][t] = 0.0;
+    for (int c = 0; c < nv / 4; c += 32) {
+        float4 w[4], v[kMoeRouteTokens];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __ldg(wr[i] + c);
+#pragma unroll
+        for (int t = 0; t < kMoeRouteTokens; ++t)
+            if (t < nt) v[t] = __ldg(xr + (int64_t)t * nv + c);
 #pragma unroll
         for (int t = 0; t < kMoeRouteTokens; ++t) {
             if (t >= nt) break;
-            float4 v[4];
+            if (a.act.sanitize) v[t] = quench4(v[t], a.act);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                v[j] = __ldg(xr + (int64_t)t * nv + i + 32 * j);
-                if (a.act.sanitize) v[j] = quench4(v[j], a.act);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                s[t] = __fma_rn((double)v[j].x, (double)w[j].x, s[t]);
-                s[t] = __fma_rn((double)v[j].y, (double)w[j].y, s[t]);
-                s[t] = __fma_rn((double)v[j].z, (double)w[j].z, s[t]);
-                s[t] = __fma_rn((double)v[j].w, (double)w[j].w, s[t]);
+            for (int i = 0; i < 4; ++i) {
+                s[i][t] = __fma_rn((double)v[t].x, (double)w[i].x, s[i][t]);
+                s[i][t] = __fma_rn((double)v[t].y, (double)w[i].y, s[i][t]);
+                s[i][t] = __fma_rn((double)v[t].z, (double)w[i].z, s[i][t]);
+                s[i][t] = __fma_rn((double)v[t].w, (double)w[i].w, s[i][t]);
             }
         }
     }
 #pragma unroll
     for (int t = 0; t < kMoeRouteTokens; ++t) {
-        const double v = warp_sum_d(s[t]);
-        if (lane == 0 && t < nt) a.logits[(int64_t)(m0 + t) * a.E + e] = __double2float_rn(v);
+        if (t >= nt) break;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const double v = warp_sum_d(s[i][t]);
+            if (lane == 0) part[warp][4 * t + i] = v;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < 16 * nt) {
+        const int t = threadIdx.x >> 4, i = threadIdx.x & 15, e = u / tgroups * kMoeWarps + i;
+        double v = 0.0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v = __dadd_rn(v, part[(i >> 2) * 4 + q][4 * t + (i & 3)]);
+        if (e < a.E) a.logits[(int64_t)(m0 + t) * a.E + e] = __double2float_rn(v);
     }
 }
 
@@ -252,95 +272,44 @@ __device__ __forceinline__ bool moe_grid_sync(unsigned *counter, unsigned n, int
     return *flag != 0;
 }
 
-// Sums of two sets of 16 weight rows (packed rows pa + r KB and pb + r KB) over
-// the column steps j0, j0 + ks, ... of 256 codes, for up to 8 NB tokens in
-// shared memory.  PD steps of weights are in flight.  A word's 16 codes enter
-// the MMA as two masked fields and, shifted by 4, two more; the fields masked in
-// place at bit 2 have an accumulator of their own (multiples of 4).
-template <int NB, int PD, bool CONV>
-__device__ __forceinline__ void moe_pair_mma(int (&acc)[2][NB][4], const uint8_t *pa, const uint8_t *pb, int KB, uint32_t x_s,
-                                             int XS, int ntok, int j0, int ks, int lane, int enc) {
-    const int g = lane >> 2, t = lane & 3, nsteps = KB >> 6;
-    const uint8_t *row[4] = {pa + (int64_t)g * KB + 16 * t, pa + (int64_t)(g + 8) * KB + 16 * t, pb + (int64_t)g * KB + 16 * t,
-                             pb + (int64_t)(g + 8) * KB + 16 * t};
-    uint32_t xr[NB];
+// Weights of one column step (256 codes) of two sets of 16 rows: rows g and g + 8
+// of each, 16 bytes of every row.
+struct MoeStep {
+    uint4 r[4];
+};
+
+// Adds one step to the sums.  A word's 16 codes enter the MMA as two masked fields
+// and, shifted by 4, two more; the fields masked in place at bit 2 have an
+// accumulator of their own (d[1], multiples of 4).  xr: this lane's token row in
+// shared memory at the step's column; xsw: its chunk swizzle.
+template <bool CONV>
+__device__ __forceinline__ void moe_step_mma(int (&d)[2][2][4], const MoeStep &w, uint32_t xr, uint32_t xsw, int enc) {
+    uint32_t c[4][4];
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-        const int m = g + 8 * nb < ntok ? g + 8 * nb : ntok - 1;  // rows past ntok: sums that are not used
-        xr[nb] = x_s + (uint32_t)(m * XS + 64 * t);
+    for (int r = 0; r < 4; ++r) {
+        c[r][0] = w.r[r].x;
+        c[r][1] = w.r[r].y;
+        c[r][2] = w.r[r].z;
+        c[r][3] = w.r[r].w;
+        if (CONV)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[r][i] = codes_to_foundry(c[r][i], enc);
     }
-    const uint32_t xsw = (uint32_t)(t & 2) << 4;
-    int d[2][2][NB][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int pr = 0; pr < 2; ++pr) {
+        const uint4 u = lds128(xr + ((uint32_t)(32 * pr) ^ xsw)), v = lds128(xr + ((uint32_t)(32 * pr + 16) ^ xsw));
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t msk = (j & 1) ? 0x0c0c0c0cu : 0x03030303u;
+            const int sh = (j & 2) * 2;
+            const uint32_t x0 = j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w;
+            const uint32_t x1 = j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) d[i][j][nb][0] = d[i][j][nb][1] = d[i][j][nb][2] = d[i][j][nb][3] = 0;
-    uint4 w[PD][4];
-#pragma unroll
-    for (int p = 0; p < PD; ++p) {
-        const int step = j0 + p * ks;
-        if (step < nsteps) {
-#pragma unroll
-            for (int r = 0; r < 4; ++r) w[p][r] = ldg_stream16(row[r] + 64 * step);
+            for (int mat = 0; mat < 2; ++mat)
+                mma_16x8x32_u8s8_pure(d[j & 1][mat], (c[2 * mat][2 * pr] >> sh) & msk, (c[2 * mat + 1][2 * pr] >> sh) & msk,
+                                      (c[2 * mat][2 * pr + 1] >> sh) & msk, (c[2 * mat + 1][2 * pr + 1] >> sh) & msk, x0, x1);
         }
     }
-    for (int base = j0; base < nsteps; base += PD * ks) {
-#pragma unroll
-        for (int p = 0; p < PD; ++p) {
-            const int step = base + p * ks;
-            if (step >= nsteps) break;
-            uint32_t c[4][4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                c[r][0] = w[p][r].x;
-                c[r][1] = w[p][r].y;
-                c[r][2] = w[p][r].z;
-                c[r][3] = w[p][r].w;
-                if (CONV)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) c[r][i] = codes_to_foundry(c[r][i], enc);
-            }
-            if (step + PD * ks < nsteps) {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) w[p][r] = ldg_stream16(row[r] + 64 * (step + PD * ks));
-            }
-            const uint32_t xo = (uint32_t)step * 256u;
-#pragma unroll
-            for (int pr = 0; pr < 2; ++pr) {
-                uint4 xt[NB][2];
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
-                    xt[nb][0] = lds128(xr[nb] + xo + ((uint32_t)(32 * pr) ^ xsw));
-                    xt[nb][1] = lds128(xr[nb] + xo + ((uint32_t)(32 * pr + 16) ^ xsw));
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t msk = (j & 1) ? 0x0c0c0c0cu : 0x03030303u;
-                    const int sh = (j & 2) * 2;
-#pragma unroll
-                    for (int mat = 0; mat < 2; ++mat) {
-                        const uint32_t a0 = (c[2 * mat][2 * pr] >> sh) & msk, a1 = (c[2 * mat + 1][2 * pr] >> sh) & msk;
-                        const uint32_t a2 = (c[2 * mat][2 * pr + 1] >> sh) & msk, a3 = (c[2 * mat + 1][2 * pr + 1] >> sh) & msk;
-#pragma unroll
-                        for (int nb = 0; nb < NB; ++nb) {
-                            const uint4 &u = xt[nb][0], &v = xt[nb][1];
-                            const uint32_t x0 = j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w;
-                            const uint32_t x1 = j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
-                            mma_16x8x32_u8s8_pure(d[j & 1][mat][nb], a0, a1, a2, a3, x0, x1);
-                        }
-                    }
-                }
-            }
-        }
-    }
-#pragma unroll
-    for (int mat = 0; mat < 2; ++mat)
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) acc[mat][nb][i] = d[0][mat][nb][i] + (d[1][mat][nb][i] >> 2);  // exact
 }
 
 // clamp(SiLU(g) u), in fp64, rounded once before the clamp
@@ -359,80 +328,130 @@ struct MoeShared {
     int ids[kMoeMaxPairs];
     float w[kMoeMaxPairs];
     int16_t sorted[kMoeMaxPairs];
-    int count[kMoeMaxExperts], first[kMoeMaxExperts];
+    int16_t count[kMoeMaxExperts], first[kMoeMaxExperts];
     MoeProblem prob[kMoeMaxProblems];
     int nprob, flag;
     MoeRed red;
 };
 
-// The strips of one run and problem.  GATE: rows n0 .. n0 + 15 of gate and up,
-// activation to a.h; else rows n0 .. n0 + 31 of down, output to a.out.
-template <int NB, bool GATE, bool CONV>
+// The strips [strip0, strip1) of one problem.  GATE: rows n0 .. n0 + 15 of gate and
+// up, activation to a.h; else rows n0 .. n0 + 31 of down, output to a.out.  Teams of
+// ks warps share a strip's column steps.  The first steps are requested, then the
+// tokens' codes are copied to shared memory.
+template <bool GATE, bool CONV>
 __device__ __forceinline__ void moe_strips(const MoeArgs &a, const MoeShared &sm, const MoeProblem &pb, int strip0, int strip1,
-                                           uint32_t x_s, int XS, int *red, int &par, int ks) {
+                                           uint32_t x_s, int *red, int ks) {
+    constexpr int PD = 2;  // steps in flight
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int team = warp / ks, kw = warp % ks, T = kMoeWarps / ks;
     const int g = lane >> 2, t = lane & 3;
-    const int N = GATE ? a.F : a.D, KB = (GATE ? a.D : a.F) / 4;
-    const int64_t base = (int64_t)pb.expert * N * KB;
-    const int count = pb.count;
-    // this lane's tokens: 8 nb + 2 t + e
-    float sv[NB][2];
-    int rv[NB][2], row[NB][2];
+    const int K = GATE ? a.D : a.F, N = GATE ? a.F : a.D, KB = K / 4, nsteps = KB / 64;
+    const int mine = (nsteps - kw + ks - 1) / ks, padded = (mine + PD - 1) / PD * PD;  // this warp's steps of a strip
+    const int64_t base = (int64_t)pb.expert * N * KB + (int64_t)g * KB + 16 * t + 64 * kw;
+    auto load = [&](MoeStep &w, int strip, int i) {  // step i of this warp's
+        const uint8_t *p = (GATE ? a.gate : a.down) + base + (int64_t)strip * ((GATE ? 16 : 32) * KB) + 64 * ks * i;
+        const uint8_t *q = GATE ? a.up + (p - a.gate) : p + 16 * KB;
+        w.r[0] = ldg_stream16(p);
+        w.r[1] = ldg_stream16(p + 8 * KB);
+        w.r[2] = ldg_stream16(q);
+        w.r[3] = ldg_stream16(q + 8 * KB);
+    };
+    MoeStep w[PD];
+    int s = strip0 + team;
+    if (s < strip1) {
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+        for (int p = 0; p < PD; ++p)
+            if (p < mine) load(w[p], s, p);
+    }
+    const int XS = gemv_x_stride(K), cpr = K >> 4;
+    for (int i = threadIdx.x; i < pb.count * cpr; i += kMoeThreads) {
+        const int r = i / cpr, c = i - r * cpr;
+        const int p = sm.sorted[pb.start + r];
+        cp_async16(x_s + (uint32_t)(r * XS + 16 * c), (GATE ? a.xq + (int64_t)(p / a.k) * K : a.hq + (int64_t)p * K) + 16 * c);
+    }
+    // this lane's tokens of a fragment: 2 t and 2 t + 1
+    float sv[2];
+    int rv[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int i = 8 * nb + 2 * t + e;
-            const int p = i < count ? sm.sorted[pb.start + i] : 0;
-            const int src = GATE ? p / a.k : p;
-            row[nb][e] = i < count ? p : -1;
-            sv[nb][e] = __ldcg((GATE ? a.sx : a.sh) + src);
-            rv[nb][e] = __ldcg((GATE ? a.rs : a.rh) + src);
+    for (int e = 0; e < 2; ++e) {
+        const int i = 2 * t + e < pb.count ? 2 * t + e : 0;
+        const int p = sm.sorted[pb.start + i], src = GATE ? p / a.k : p;
+        sv[e] = __ldcg((GATE ? a.sx : a.sh) + src);
+        rv[e] = __ldcg((GATE ? a.rs : a.rh) + src);
+    }
+    cp_async_wait_all();
+    __syncthreads();
+    // token g of the problem (past the last: sums that are not used)
+    const uint32_t xr = x_s + (uint32_t)((g < pb.count ? g : pb.count - 1) * XS + 64 * t + 256 * kw);
+    const uint32_t xsw = (uint32_t)(t & 2) << 4;
+    int par = 0;
+    for (; s < strip1; s += T) {
+        int d[2][2][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[0][0][i] = d[0][1][i] = d[1][0][i] = d[1][1][i] = 0;
+        for (int i0 = 0; i0 < padded; i0 += PD) {
+#pragma unroll
+            for (int p = 0; p < PD; ++p) {
+                const int i = i0 + p;
+                if (i < mine) moe_step_mma<CONV>(d, w[p], xr + (uint32_t)(256 * ks * i), xsw, a.enc);
+                // the step PD ahead: of this strip, or of this team's next
+                if (i + PD < padded) {
+                    if (i + PD < mine) load(w[p], s, i + PD);
+                } else if (s + T < strip1 && p < mine) {
+                    load(w[p], s + T, p);
+                }
+            }
         }
-    for (int s = strip0 + team; s < strip1; s += T) {
-        const int n0 = s * (GATE ? 16 : 32);
-        const uint8_t *pa = (GATE ? a.gate : a.down) + base + (int64_t)n0 * KB;
-        const uint8_t *pbk = GATE ? a.up + base + (int64_t)n0 * KB : pa + 16 * (int64_t)KB;
-        int acc[2][NB][4];
-        moe_pair_mma<NB, NB == 1 ? 4 : 2, CONV>(acc, pa, pbk, KB, x_s, XS, count, kw, ks, lane, a.enc);
+        int acc[2][4];
+#pragma unroll
+        for (int mat = 0; mat < 2; ++mat)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[mat][i] = d[0][mat][i] + (d[1][mat][i] >> 2);  // exact
+        int *slots = red + par * (kMoeWarps * kMoeSlot);
         if (ks > 1) {
-            int *rb = red + par * (kMoeRedBytes / 8);
             if (kw != 0) {
 #pragma unroll
-                for (int i = 0; i < 8 * NB; ++i) rb[(warp * 16 + i) * 32 + lane] = acc[i / (4 * NB)][i / 4 % NB][i % 4];
+                for (int i = 0; i < 8; ++i) slots[warp * kMoeSlot + i * 32 + lane] = acc[i >> 2][i & 3];
             }
             bar_sync_n(1 + team, 32 * ks);
             if (kw == 0) {
                 for (int w2 = warp + 1; w2 < warp + ks; ++w2)
 #pragma unroll
-                    for (int i = 0; i < 8 * NB; ++i) acc[i / (4 * NB)][i / 4 % NB][i % 4] += rb[(w2 * 16 + i) * 32 + lane];
+                    for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] += slots[w2 * kMoeSlot + i * 32 + lane];
             }
             par ^= 1;
         }
         if (kw != 0) continue;
-        // sum c of a fragment: row g (+ 8 for c >= 2), token 8 nb + 2 t + (c & 1)
-        const float *g1 = GATE ? a.gate_gamma : a.down_gamma, *g2 = GATE ? a.up_gamma : a.down_gamma;
+        // The projections' values pass through this warp's own slot, so that the
+        // lanes share what follows evenly and stores cover whole rows' stretches:
+        // value (mat, row, token) at [mat][token / 2][(16 (token % 2) + row + 8 (token / 2)) % 32].
+        const int n0 = s * (GATE ? 16 : 32);
+        const float *g1 = GATE ? a.gate_gamma : a.down_gamma, *g2 = GATE ? a.up_gamma : a.down_gamma + (a.per_row ? 16 : 0);
+        float *val = reinterpret_cast<float *>(slots + warp * kMoeSlot);
+        __syncwarp();  // the slot's last readers are done
 #pragma unroll
         for (int hi = 0; hi < 2; ++hi) {
-            const int n = n0 + g + 8 * hi;
-            const float ga = __ldg(g1 + (a.per_row ? (int64_t)pb.expert * N + n : pb.expert));
-            const float gb = __ldg(g2 + (a.per_row ? (int64_t)pb.expert * N + n + (GATE ? 0 : 16) : pb.expert));
+            const int64_t n = a.per_row ? (int64_t)pb.expert * N + n0 + g + 8 * hi : pb.expert;
+            const float ga = __ldg(g1 + n), gb = __ldg(g2 + n);
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int p = row[nb][e], c = 2 * hi + e;
-                    if (p < 0) continue;
-                    const float va = __fmul_rn(__int2float_rn(acc[0][nb][c] - rv[nb][e]), __fmul_rn(ga, sv[nb][e]));
-                    const float vb = __fmul_rn(__int2float_rn(acc[1][nb][c] - rv[nb][e]), __fmul_rn(gb, sv[nb][e]));
-                    if (GATE) {
-                        a.h[(int64_t)p * N + n] = moe_act(va, vb, a.clamp_val);
-                    } else {
-                        a.out[(int64_t)p * N + n] = va;
-                        a.out[(int64_t)p * N + n + 16] = vb;
-                    }
-                }
+            for (int e = 0; e < 2; ++e) {
+                const int c = 2 * hi + e, at = 32 * t + ((16 * e + g + 8 * hi + 8 * t) & 31);
+                val[at] = __fmul_rn(__int2float_rn(acc[0][c] - rv[e]), __fmul_rn(ga, sv[e]));
+                val[128 + at] = __fmul_rn(__int2float_rn(acc[1][c] - rv[e]), __fmul_rn(gb, sv[e]));
+            }
+        }
+        __syncwarp();
+        if (GATE) {
+            for (int i = lane; i < 16 * pb.count; i += 32) {
+                const int tok = i >> 4, row = i & 15, h = tok >> 1;
+                const int at = 32 * h + ((16 * (tok & 1) + row + 8 * h) & 31);
+                a.h[(int64_t)sm.sorted[pb.start + tok] * N + n0 + row] = moe_act(val[at], val[128 + at], a.clamp_val);
+            }
+        } else {
+            for (int tok = 0; tok < pb.count; ++tok) {
+                const int h = tok >> 1, at = 32 * h + ((16 * (tok & 1) + (lane & 15) + 8 * h) & 31);
+                a.out[(int64_t)sm.sorted[pb.start + tok] * N + n0 + lane] = val[128 * (lane >> 4) + at];
+            }
         }
     }
 }
@@ -448,29 +467,13 @@ __device__ __forceinline__ void moe_contract(const MoeArgs &a, MoeShared &sm, ui
     // warps per strip: as many as keep every warp busy when runs are short
     int ks = kMoeWarps;
     while (ks > 1 && (kMoeWarps / ks < run || ks > K / 256)) ks >>= 1;
-    const int XS = gemv_x_stride(K);
     int *red = reinterpret_cast<int *>(dyn);
-    uint8_t *xb = dyn + kMoeRedBytes;
-    const uint32_t x_s = smem_u32(xb);
-    int par = 0;
+    const uint32_t x_s = smem_u32(dyn + kMoeRedBytes);
     for (int64_t s = s0; s < s1;) {
         const int q = (int)(s / spp);
-        const MoeProblem pb = sm.prob[q];
-        const int64_t end = s1 < (int64_t)(q + 1) * spp ? s1 : (int64_t)(q + 1) * spp;
-        __syncthreads();  // the previous problem's tokens have been read
-        const int cpr = K >> 4;
-        for (int i = threadIdx.x; i < pb.count * cpr; i += kMoeThreads) {
-            const int r = i / cpr, c = i - r * cpr;
-            const int p = sm.sorted[pb.start + r];
-            cp_async16(x_s + (uint32_t)(r * XS + 16 * c), (GATE ? a.xq + (int64_t)(p / a.k) * K : a.hq + (int64_t)p * K) + 16 * c);
-        }
-        cp_async_wait_all();
-        __syncthreads();
-        const int a0 = (int)(s - (int64_t)q * spp), a1 = (int)(end - (int64_t)q * spp);
-        if (pb.count <= 8)
-            moe_strips<1, GATE, CONV>(a, sm, pb, a0, a1, x_s, XS, red, par, ks);
-        else
-            moe_strips<2, GATE, CONV>(a, sm, pb, a0, a1, x_s, XS, red, par, ks);
+        const int64_t first = (int64_t)q * spp, end = s1 < first + spp ? s1 : first + spp;
+        __syncthreads();  // the previous problem's tokens and slots have been read
+        moe_strips<GATE, CONV>(a, sm, sm.prob[q], (int)(s - first), (int)(end - first), x_s, red, ks);
         s = end;
     }
 }
@@ -501,34 +504,37 @@ __global__ void __launch_bounds__(kMoeThreads, 1) tq_moe_experts_kernel(const __
             l[i] = e < a.E ? __ldcg(a.logits + (int64_t)m * a.E + e) : 0.0f;
             key[i] = e < a.E ? moe_key(l[i]) : 0u;
         }
-        uint32_t used = 0;  // bit i: expert lane + 32 i is chosen (or does not exist)
+        // this lane's best expert not chosen yet (key, index; the lowest index of equals)
+        uint32_t used = 0, best = 0, at = 0xffffu;
+        float val = 0.0f, top = 0.0f, mine = 0.0f;  // its logit; the largest logit; the logit of slot `lane`
+        auto scan = [&]() {
+            best = 0;
+            at = 0xffffu;
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            if (lane + 32 * i >= a.E) used |= 1u << i;
-        float top = 0.0f, mine = 0.0f;  // the largest logit; the logit of slot `lane`
-        int my_id = 0;
-        for (int j = 0; j < a.k; ++j) {
-            // the largest key (+ 1, so that an unused NaN beats nothing), then the lowest index
-            uint32_t best = 0;
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (!(used >> i & 1u)) best = best > key[i] ? best : key[i];
-            best = __reduce_max_sync(0xffffffffu, best);
-            uint32_t at = 0xffffu;
-            float val = 0.0f;
-#pragma unroll
-            for (int i = V - 1; i >= 0; --i)
-                if (!(used >> i & 1u) && key[i] == best) {
+            for (int i = 0; i < V; ++i) {
+                if (32 * i >= a.E) break;
+                const bool free = lane + 32 * i < a.E && !(used >> i & 1u);
+                if (free && (at == 0xffffu || key[i] > best)) {
+                    best = key[i];
                     at = (uint32_t)(lane + 32 * i);
                     val = l[i];
                 }
-            const uint32_t id = __reduce_min_sync(0xffffffffu, at);
-            val = __shfl_sync(0xffffffffu, val, id & 31);
-            if ((int)(id & 31) == lane) used |= 1u << (id >> 5);
-            if (j == 0) top = val;
+            }
+        };
+        scan();
+        int my_id = 0;
+        for (int j = 0; j < a.k; ++j) {
+            const uint32_t most = __reduce_max_sync(0xffffffffu, best);
+            const uint32_t id = __reduce_min_sync(0xffffffffu, best == most ? at : 0xffffu);
+            const float v = __shfl_sync(0xffffffffu, val, id & 31);
+            if (j == 0) top = v;
             if (lane == j) {
                 my_id = (int)id;
-                mine = val;
+                mine = v;
+            }
+            if ((int)(id & 31) == lane) {
+                used |= 1u << (id >> 5);
+                scan();
             }
         }
         double den;
@@ -552,57 +558,69 @@ __global__ void __launch_bounds__(kMoeThreads, 1) tq_moe_experts_kernel(const __
             }
         }
     }
-    for (int e = threadIdx.x; e < a.E; e += kMoeThreads) sm.count[e] = 0;
+    // Pairs by expert, in order (every CTA must come to the same grouping).  Warps
+    // rank the pairs of 32 at a time among those of the same expert and count them;
+    // a thread per expert turns its counts into offsets.
+    const int nch = (P + 31) / 32;
+    uint16_t *counts = reinterpret_cast<uint16_t *>(dyn);  // [nch][E]
+    for (int i = threadIdx.x; i < nch * a.E; i += kMoeThreads) counts[i] = 0;
     __syncthreads();
-    // Pairs by expert, in order (every CTA must come to the same grouping): warp 0
-    // ranks 32 pairs at a time among those of the same expert.
-    if (warp == 0) {
-        for (int pass = 0; pass < 2; ++pass) {
-            for (int p0 = 0; p0 < P; p0 += 32) {
-                const int p = p0 + lane;
-                const int id = p < P ? sm.ids[p] : -1;
-                const uint32_t same = __match_any_sync(0xffffffffu, id);
-                const int rank = __popc(same & ((1u << lane) - 1u));
-                const int before = id >= 0 ? sm.count[id] : 0;
-                __syncwarp();
-                if (id >= 0) {
-                    if (pass == 1) sm.sorted[sm.first[id] + before + rank] = (int16_t)p;
-                    if (rank == 0) sm.count[id] = before + __popc(same);
-                }
-                __syncwarp();
-            }
-            if (pass == 0) {
-                int at = 0, np = 0;  // running sums over experts
-                for (int e0 = 0; e0 < a.E; e0 += 32) {
-                    const int e = e0 + lane;
-                    const int c = e < a.E ? sm.count[e] : 0, n = (c + kMoeChunk - 1) / kMoeChunk;
-                    int cs = c, ns = n;
+    int id_of[2] = {-1, -1}, rank[2] = {0, 0};  // chunks warp and warp + 16
 #pragma unroll
-                    for (int off = 1; off < 32; off <<= 1) {
-                        const int v = __shfl_up_sync(0xffffffffu, cs, off), u = __shfl_up_sync(0xffffffffu, ns, off);
-                        if (lane >= off) {
-                            cs += v;
-                            ns += u;
-                        }
-                    }
-                    if (e < a.E) {
-                        sm.first[e] = at + cs - c;
-                        for (int i = 0; i < n; ++i) {
-                            MoeProblem pb;
-                            pb.expert = (int16_t)e;
-                            pb.start = (int16_t)(at + cs - c + i * kMoeChunk);
-                            pb.count = (int16_t)(c - i * kMoeChunk < kMoeChunk ? c - i * kMoeChunk : kMoeChunk);
-                            sm.prob[np + ns - n + i] = pb;
-                        }
-                        sm.count[e] = 0;
-                    }
-                    at += __shfl_sync(0xffffffffu, cs, 31);
-                    np += __shfl_sync(0xffffffffu, ns, 31);
-                }
-                if (lane == 0) sm.nprob = np;
-                __syncwarp();
-            }
+    for (int c = 0; c < 2; ++c) {
+        const int ch = warp + kMoeWarps * c, p = 32 * ch + lane;
+        if (ch >= nch) break;
+        const int id = p < P ? sm.ids[p] : -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, id);
+        id_of[c] = id;
+        rank[c] = __popc(same & ((1u << lane) - 1u));
+        if (id >= 0 && rank[c] == 0) counts[ch * a.E + id] = (uint16_t)__popc(same);
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < a.E) {
+        int n = 0;
+        for (int ch = 0; ch < nch; ++ch) {
+            const int c = counts[ch * a.E + threadIdx.x];
+            counts[ch * a.E + threadIdx.x] = (uint16_t)n;
+            n += c;
         }
+        sm.count[threadIdx.x] = (int16_t)n;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int at = 0, np = 0;  // running sums over experts
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            const int e = e0 + lane;
+            const int c = e < a.E ? sm.count[e] : 0, n = (c + kMoeChunk - 1) / kMoeChunk;
+            int cs = c, ns = n;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, cs, off), u = __shfl_up_sync(0xffffffffu, ns, off);
+                if (lane >= off) {
+                    cs += v;
+                    ns += u;
+                }
+            }
+            if (e < a.E) {
+                sm.first[e] = (int16_t)(at + cs - c);
+                for (int i = 0; i < n; ++i) {
+                    MoeProblem pb;
+                    pb.expert = (int16_t)e;
+                    pb.start = (int16_t)(at + cs - c + i * kMoeChunk);
+                    pb.count = (int16_t)(c - i * kMoeChunk < kMoeChunk ? c - i * kMoeChunk : kMoeChunk);
+                    sm.prob[np + ns - n + i] = pb;
+                }
+            }
+            at += __shfl_sync(0xffffffffu, cs, 31);
+            np += __shfl_sync(0xffffffffu, ns, 31);
+        }
+        if (lane == 0) sm.nprob = np;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        const int ch = warp + kMoeWarps * c;
+        if (id_of[c] >= 0) sm.sorted[sm.first[id_of[c]] + counts[ch * a.E + id_of[c]] + rank[c]] = (int16_t)(32 * ch + lane);
     }
     __syncthreads();
 
