@@ -603,22 +603,24 @@ inline bool moe_shape_ok(int64_t M, int64_t D, int64_t F, int64_t E, int64_t k) 
            F % 512 == 0 && E >= 1 && E <= kMoeMaxExperts && k >= 1 && k <= kMoeMaxTopk && k <= E;
 }
 
-template <bool CONV>
+constexpr int kMoeRingK = 4096;  // longest token rows that leave room for a ring of four steps
+
+template <bool CONV, int PD>
 tq_status launch_moe_experts(const MoeArgs &a, int sms, cudaStream_t st) {
     static std::atomic<int> attr_done[kMaxDevices];
-    constexpr int kMost = kMoeRedBytes + kMoeChunk * (kMoeMaxK + 128);
-    if (tq_status e = set_smem_once(tq_moe_experts_kernel<CONV>, kMost, attr_done)) return e;
+    constexpr int kFixed = kMoeRedBytes + kMoeWarps * PD * 2048, kMostK = PD == 4 ? kMoeRingK : kMoeMaxK;
+    if (tq_status e = set_smem_once(tq_moe_experts_kernel<CONV, PD>, kFixed + kMoeChunk * (kMostK + 128), attr_done)) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)sms);
     cfg.blockDim = dim3(kMoeThreads);
-    cfg.dynamicSmemBytes = (size_t)(kMoeRedBytes + kMoeChunk * gemv_x_stride(a.D > a.F ? a.D : a.F));
+    cfg.dynamicSmemBytes = (size_t)(kFixed + kMoeChunk * gemv_x_stride(a.D > a.F ? a.D : a.F));
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;  // its CTAs wait for one another
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tq_moe_experts_kernel<CONV>, a) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, tq_moe_experts_kernel<CONV, PD>, a) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
 // ---------------------------------------------------------------------------
@@ -1450,7 +1452,9 @@ tq_status tq_moe_swiglu(const float *x, int64_t M, int64_t d_model, int64_t d_ff
     cudaStream_t st = cs(stream);
     const int64_t units = router ? (n_experts + kMoeWarps - 1) / kMoeWarps * ((M + kMoeRouteTokens - 1) / kMoeRouteTokens) : 0;
     if (tq_status e = launch_pdl(tq_moe_route_kernel, dim3((unsigned)(M + units)), dim3(kMoeThreads), 0, st, a)) return e;
-    return enc != kEncFoundry ? launch_moe_experts<true>(a, sms, st) : launch_moe_experts<false>(a, sms, st);
+    if (d_model <= kMoeRingK && d_ffn <= kMoeRingK)
+        return enc != kEncFoundry ? launch_moe_experts<true, 4>(a, sms, st) : launch_moe_experts<false, 4>(a, sms, st);
+    return enc != kEncFoundry ? launch_moe_experts<true, 3>(a, sms, st) : launch_moe_experts<false, 3>(a, sms, st);
 }
 
 tq_status tq_selftest_wait_timeout(uint64_t limit_ns, int sleeping, tq_stream_t stream) {

@@ -32,10 +32,15 @@
 //       down       strips of 32 rows, runs as before.
 //       sum        y from the pairs' outputs, slots in order: no atomics, and
 //                  the result does not depend on how pairs were grouped.
-//   A warp streams its strips' weights from HBM into registers, two column steps
-//   (4 KB) ahead and across strips, and contracts them with mma.sync (u8 codes x
-//   s8): for 8 tokens the tensor rate is no bound, and no shared memory is spent
-//   on bytes that are used once.
+//   A warp streams its strips' weights from HBM by asynchronous copies into a ring
+//   of its own, three or four column steps (of 2 KB) ahead and across strips; a lane
+//   reads only what it copied itself, so the ring needs no barrier.  They are
+//   contracted with mma.sync (u8 codes x s8), whose rate is no bound here; the logic
+//   operations that spread the codes are, at half the rate of the others, which is
+//   why a code stays where it is in its byte: field j is masked in place, counts
+//   4^j-fold and has sums of its own.  (Spreading them to fp16 for the twice as wide
+//   fp16 mma.sync took more of them: 149 us instead of 127 at 64 x 2048 x 1536 of
+//   128 experts.)
 #pragma once
 
 #include "tq_act.cuh"
@@ -272,25 +277,21 @@ __device__ __forceinline__ bool moe_grid_sync(unsigned *counter, unsigned n, int
     return *flag != 0;
 }
 
-// Weights of one column step (256 codes) of two sets of 16 rows: rows g and g + 8
-// of each, 16 bytes of every row.
-struct MoeStep {
-    uint4 r[4];
-};
-
-// Adds one step to the sums.  A word's 16 codes enter the MMA as two masked fields
-// and, shifted by 4, two more; the fields masked in place at bit 2 have an
-// accumulator of their own (d[1], multiples of 4).  xr: this lane's token row in
-// shared memory at the step's column; xsw: its chunk swizzle.
+// Adds one column step (256 codes) of two sets of 16 rows to the sums.  w: this
+// lane's 16 bytes of rows g and g + 8 of each set, in shared memory 512 bytes
+// apart.  Field j of a word enters the MMA masked in place (code times 4^j) and
+// has an accumulator d[j] of its own.  xr: this lane's token row in shared memory
+// at the step's column; xsw: its chunk swizzle.
 template <bool CONV>
-__device__ __forceinline__ void moe_step_mma(int (&d)[2][2][4], const MoeStep &w, uint32_t xr, uint32_t xsw, int enc) {
+__device__ __forceinline__ void moe_step_mma(int (&d)[4][2][4], uint32_t w, uint32_t xr, uint32_t xsw, int enc) {
     uint32_t c[4][4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-        c[r][0] = w.r[r].x;
-        c[r][1] = w.r[r].y;
-        c[r][2] = w.r[r].z;
-        c[r][3] = w.r[r].w;
+        const uint4 v = lds128(w + 512 * r);
+        c[r][0] = v.x;
+        c[r][1] = v.y;
+        c[r][2] = v.z;
+        c[r][3] = v.w;
         if (CONV)
 #pragma unroll
             for (int i = 0; i < 4; ++i) c[r][i] = codes_to_foundry(c[r][i], enc);
@@ -300,16 +301,21 @@ __device__ __forceinline__ void moe_step_mma(int (&d)[2][2][4], const MoeStep &w
         const uint4 u = lds128(xr + ((uint32_t)(32 * pr) ^ xsw)), v = lds128(xr + ((uint32_t)(32 * pr + 16) ^ xsw));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const uint32_t msk = (j & 1) ? 0x0c0c0c0cu : 0x03030303u;
-            const int sh = (j & 2) * 2;
+            const uint32_t msk = 0x03030303u << (2 * j);
             const uint32_t x0 = j == 0 ? u.x : j == 1 ? u.y : j == 2 ? u.z : u.w;
             const uint32_t x1 = j == 0 ? v.x : j == 1 ? v.y : j == 2 ? v.z : v.w;
 #pragma unroll
             for (int mat = 0; mat < 2; ++mat)
-                mma_16x8x32_u8s8_pure(d[j & 1][mat], (c[2 * mat][2 * pr] >> sh) & msk, (c[2 * mat + 1][2 * pr] >> sh) & msk,
-                                      (c[2 * mat][2 * pr + 1] >> sh) & msk, (c[2 * mat + 1][2 * pr + 1] >> sh) & msk, x0, x1);
+                mma_16x8x32_u8s8_pure(d[j][mat], c[2 * mat][2 * pr] & msk, c[2 * mat + 1][2 * pr] & msk,
+                                      c[2 * mat][2 * pr + 1] & msk, c[2 * mat + 1][2 * pr + 1] & msk, x0, x1);
         }
     }
+}
+
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait_groups() {  // all but the last N groups have landed
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // clamp(SiLU(g) u), in fp64, rounded once before the clamp
@@ -336,38 +342,39 @@ struct MoeShared {
 
 // The strips [strip0, strip1) of one problem.  GATE: rows n0 .. n0 + 15 of gate and
 // up, activation to a.h; else rows n0 .. n0 + 31 of down, output to a.out.  Teams of
-// ks warps share a strip's column steps.  The first steps are requested, then the
-// tokens' codes are copied to shared memory.
-template <bool GATE, bool CONV>
+// ks warps share a strip's column steps.  PD: steps in the ring.
+template <bool GATE, bool CONV, int PD>
 __device__ __forceinline__ void moe_strips(const MoeArgs &a, const MoeShared &sm, const MoeProblem &pb, int strip0, int strip1,
-                                           uint32_t x_s, int *red, int ks) {
-    constexpr int PD = 2;  // steps in flight
+                                           uint32_t x_s, uint32_t ring_s, int *red, int ks) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int team = warp / ks, kw = warp % ks, T = kMoeWarps / ks;
     const int g = lane >> 2, t = lane & 3;
     const int K = GATE ? a.D : a.F, N = GATE ? a.F : a.D, KB = K / 4, nsteps = KB / 64;
     const int mine = (nsteps - kw + ks - 1) / ks, padded = (mine + PD - 1) / PD * PD;  // this warp's steps of a strip
     const int64_t base = (int64_t)pb.expert * N * KB + (int64_t)g * KB + 16 * t + 64 * kw;
-    auto load = [&](MoeStep &w, int strip, int i) {  // step i of this warp's
+    const uint32_t ring = ring_s + (uint32_t)(warp * PD * 2048 + 16 * lane);
+    auto load = [&](int slot, int strip, int i) {  // step i of this warp's
         const uint8_t *p = (GATE ? a.gate : a.down) + base + (int64_t)strip * ((GATE ? 16 : 32) * KB) + 64 * ks * i;
         const uint8_t *q = GATE ? a.up + (p - a.gate) : p + 16 * KB;
-        w.r[0] = ldg_stream16(p);
-        w.r[1] = ldg_stream16(p + 8 * KB);
-        w.r[2] = ldg_stream16(q);
-        w.r[3] = ldg_stream16(q + 8 * KB);
+        const uint32_t dst = ring + (uint32_t)(slot * 2048);
+        cp_async16(dst, p);
+        cp_async16(dst + 512, p + 8 * KB);
+        cp_async16(dst + 1024, q);
+        cp_async16(dst + 1536, q + 8 * KB);
     };
-    MoeStep w[PD];
-    int s = strip0 + team;
-    if (s < strip1) {
-#pragma unroll
-        for (int p = 0; p < PD; ++p)
-            if (p < mine) load(w[p], s, p);
-    }
+    // one group for the tokens' codes, one per step
     const int XS = gemv_x_stride(K), cpr = K >> 4;
     for (int i = threadIdx.x; i < pb.count * cpr; i += kMoeThreads) {
         const int r = i / cpr, c = i - r * cpr;
         const int p = sm.sorted[pb.start + r];
         cp_async16(x_s + (uint32_t)(r * XS + 16 * c), (GATE ? a.xq + (int64_t)(p / a.k) * K : a.hq + (int64_t)p * K) + 16 * c);
+    }
+    cp_async_commit();
+    int s = strip0 + team;
+#pragma unroll
+    for (int p = 0; p < PD; ++p) {
+        if (s < strip1 && p < mine) load(p, s, p);
+        cp_async_commit();
     }
     // this lane's tokens of a fragment: 2 t and 2 t + 1
     float sv[2];
@@ -379,34 +386,39 @@ __device__ __forceinline__ void moe_strips(const MoeArgs &a, const MoeShared &sm
         sv[e] = __ldcg((GATE ? a.sx : a.sh) + src);
         rv[e] = __ldcg((GATE ? a.rs : a.rh) + src);
     }
-    cp_async_wait_all();
+    cp_async_wait_groups<PD>();
     __syncthreads();
     // token g of the problem (past the last: sums that are not used)
     const uint32_t xr = x_s + (uint32_t)((g < pb.count ? g : pb.count - 1) * XS + 64 * t + 256 * kw);
     const uint32_t xsw = (uint32_t)(t & 2) << 4;
     int par = 0;
     for (; s < strip1; s += T) {
-        int d[2][2][4];
+        int d[4][2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[0][0][i] = d[0][1][i] = d[1][0][i] = d[1][1][i] = 0;
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[j][0][i] = d[j][1][i] = 0;
         for (int i0 = 0; i0 < padded; i0 += PD) {
 #pragma unroll
             for (int p = 0; p < PD; ++p) {
                 const int i = i0 + p;
-                if (i < mine) moe_step_mma<CONV>(d, w[p], xr + (uint32_t)(256 * ks * i), xsw, a.enc);
+                cp_async_wait_groups<PD - 1>();
+                if (i < mine) moe_step_mma<CONV>(d, ring + (uint32_t)(p * 2048), xr + (uint32_t)(256 * ks * i), xsw, a.enc);
                 // the step PD ahead: of this strip, or of this team's next
                 if (i + PD < padded) {
-                    if (i + PD < mine) load(w[p], s, i + PD);
+                    if (i + PD < mine) load(p, s, i + PD);
                 } else if (s + T < strip1 && p < mine) {
-                    load(w[p], s + T, p);
+                    load(p, s + T, p);
                 }
+                cp_async_commit();
             }
         }
         int acc[2][4];
 #pragma unroll
         for (int mat = 0; mat < 2; ++mat)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[mat][i] = d[0][mat][i] + (d[1][mat][i] >> 2);  // exact
+            for (int i = 0; i < 4; ++i)  // exact: d[j] is a multiple of 4^j
+                acc[mat][i] = d[0][mat][i] + (d[1][mat][i] >> 2) + (d[2][mat][i] >> 4) + (d[3][mat][i] >> 6);
         int *slots = red + par * (kMoeWarps * kMoeSlot);
         if (ks > 1) {
             if (kw != 0) {
@@ -457,7 +469,7 @@ __device__ __forceinline__ void moe_strips(const MoeArgs &a, const MoeShared &sm
 }
 
 // One contraction phase over all problems: this CTA's run of strips.
-template <bool GATE, bool CONV>
+template <bool GATE, bool CONV, int PD>
 __device__ __forceinline__ void moe_contract(const MoeArgs &a, MoeShared &sm, uint8_t *dyn) {
     const int K = GATE ? a.D : a.F, N = GATE ? a.F : a.D;
     const int spp = N / (GATE ? 16 : 32);
@@ -468,17 +480,19 @@ __device__ __forceinline__ void moe_contract(const MoeArgs &a, MoeShared &sm, ui
     int ks = kMoeWarps;
     while (ks > 1 && (kMoeWarps / ks < run || ks > K / 256)) ks >>= 1;
     int *red = reinterpret_cast<int *>(dyn);
-    const uint32_t x_s = smem_u32(dyn + kMoeRedBytes);
+    const uint32_t ring_s = smem_u32(dyn + kMoeRedBytes), x_s = ring_s + kMoeWarps * PD * 2048;
     for (int64_t s = s0; s < s1;) {
         const int q = (int)(s / spp);
         const int64_t first = (int64_t)q * spp, end = s1 < first + spp ? s1 : first + spp;
         __syncthreads();  // the previous problem's tokens and slots have been read
-        moe_strips<GATE, CONV>(a, sm, sm.prob[q], (int)(s - first), (int)(end - first), x_s, red, ks);
+        moe_strips<GATE, CONV, PD>(a, sm, sm.prob[q], (int)(s - first), (int)(end - first), x_s, ring_s, red, ks);
         s = end;
     }
+    cp_async_wait_groups<0>();
 }
 
-template <bool CONV>
+// PD: column steps in each warp's ring (4, or 3 where longer token rows need the room).
+template <bool CONV, int PD>
 __global__ void __launch_bounds__(kMoeThreads, 1) tq_moe_experts_kernel(const __grid_constant__ MoeArgs a) {
     extern __shared__ __align__(128) uint8_t dyn[];
     __shared__ MoeShared sm;
@@ -625,7 +639,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) tq_moe_experts_kernel(const __
     __syncthreads();
 
     // ---------------- gate, up, activation ----------------
-    moe_contract<true, CONV>(a, sm, dyn);
+    moe_contract<true, CONV, PD>(a, sm, dyn);
     if (!moe_grid_sync(a.barrier, 1, &sm.flag)) return;
     // ---------------- rotation and codes of every pair ----------------
     {
@@ -644,7 +658,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) tq_moe_experts_kernel(const __
     }
     if (!moe_grid_sync(a.barrier, 2, &sm.flag)) return;
     // ---------------- down ----------------
-    moe_contract<false, CONV>(a, sm, dyn);
+    moe_contract<false, CONV, PD>(a, sm, dyn);
     if (!moe_grid_sync(a.barrier, 3, &sm.flag)) return;
     // ---------------- sum over the slots ----------------
     const int nv = a.D / 4;
