@@ -609,11 +609,11 @@ template <bool CONV, int PD>
 tq_status launch_moe_experts(const MoeArgs &a, int sms, cudaStream_t st) {
     static std::atomic<int> attr_done[kMaxDevices];
     constexpr int kFixed = kMoeRedBytes + kMoeWarps * PD * 2048, kMostK = PD == 4 ? kMoeRingK : kMoeMaxK;
-    if (tq_status e = set_smem_once(tq_moe_experts_kernel<CONV, PD>, kFixed + kMoeChunk * (kMostK + 128), attr_done)) return e;
+    if (tq_status e = set_smem_once(tq_moe_experts_kernel<CONV, PD>, kFixed + 2 * kMoeChunk * (kMostK + 128), attr_done)) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)sms);
     cfg.blockDim = dim3(kMoeThreads);
-    cfg.dynamicSmemBytes = (size_t)(kFixed + kMoeChunk * gemv_x_stride(a.D > a.F ? a.D : a.F));
+    cfg.dynamicSmemBytes = (size_t)(kFixed + 2 * kMoeChunk * gemv_x_stride(a.D > a.F ? a.D : a.F));
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeCooperative;  // its CTAs wait for one another
@@ -1454,7 +1454,7 @@ tq_status tq_moe_swiglu(const float *x, int64_t M, int64_t d_model, int64_t d_ff
     if (tq_status e = launch_pdl(tq_moe_route_kernel, dim3((unsigned)(M + units)), dim3(kMoeThreads), 0, st, a)) return e;
     if (d_model <= kMoeRingK && d_ffn <= kMoeRingK)
         return enc != kEncFoundry ? launch_moe_experts<true, 4>(a, sms, st) : launch_moe_experts<false, 4>(a, sms, st);
-    return enc != kEncFoundry ? launch_moe_experts<true, 3>(a, sms, st) : launch_moe_experts<false, 3>(a, sms, st);
+    return enc != kEncFoundry ? launch_moe_experts<true, 2>(a, sms, st) : launch_moe_experts<false, 2>(a, sms, st);
 }
 
 tq_status tq_selftest_wait_timeout(uint64_t limit_ns, int sleeping, tq_stream_t stream) {

@@ -20,9 +20,9 @@
 //   tq_moe_route_kernel: a CTA per token quantises it; the other CTAs compute the
 //     logits of 16 experts and four tokens each.
 //   tq_moe_experts_kernel: one CTA per SM, launched cooperatively (all CTAs
-//     resident), with three grid-wide barriers between its phases:
-//       choice     every CTA picks every token's experts (cheaper than another
-//                  barrier) and sorts the (token, slot) pairs by expert; an expert
+//     resident), with grid-wide barriers between its phases:
+//       choice     every CTA picks every token's experts (for up to 16 tokens that is
+//                  cheaper than another barrier) and sorts the (token, slot) pairs by expert; an expert
 //                  and up to 8 of its pairs are one "problem".
 //       gate, up   a strip is 16 rows of both matrices, so that the activation
 //                  follows in registers.  The strips of all problems are split
@@ -33,8 +33,9 @@
 //       sum        y from the pairs' outputs, slots in order: no atomics, and
 //                  the result does not depend on how pairs were grouped.
 //   A warp streams its strips' weights from HBM by asynchronous copies into a ring
-//   of its own, three or four column steps (of 2 KB) ahead and across strips; a lane
-//   reads only what it copied itself, so the ring needs no barrier.  They are
+//   of its own, two or four column steps (of 2 KB) ahead, across strips and problems,
+//   and into the down phase from before the rotation; a lane reads only what it
+//   copied itself, so the ring needs no barrier.  They are
 //   contracted with mma.sync (u8 codes x s8), whose rate is no bound here; the logic
 //   operations that spread the codes are, at half the rate of the others, which is
 //   why a code stays where it is in its byte: field j is masked in place, counts
@@ -58,7 +59,7 @@ constexpr int kMoeMaxProblems = kMoeMaxExperts + kMoeMaxPairs / kMoeChunk;
 constexpr int kMoeMaxK = 8192;  // d_model, d_ffn: 16 blocks of 512, one per warp
 constexpr int kMoeRouteTokens = 4;
 constexpr int kMoeSlot = 8 * 32;  // 32-bit words of a warp's exchange slot
-constexpr int kMoeRedBytes = 2 * kMoeWarps * kMoeSlot * 4;
+constexpr int kMoeRedBytes = kMoeWarps * kMoeSlot * 4;
 static_assert(kMoeRedBytes >= kMoeMaxPairs / 32 * kMoeMaxExperts * 2, "the pair counts fit the exchange slots");
 
 struct MoeArgs {
@@ -108,14 +109,18 @@ __device__ __forceinline__ void moe_rot_quant(float (&f)[16], int wt, int nw, in
         for (int i = 0; i < 16; ++i) f[i] = quench(f[i], p.eta_max);
     }
     if (p.rmsnorm) {
-        double ss = 0.0;
+        double sq[4] = {0.0, 0.0, 0.0, 0.0};  // four chains: this is on the critical path
 #pragma unroll
-        for (int i = 0; i < 16; ++i) ss = __fma_rn((double)f[i], (double)f[i], ss);
-        ss = warp_sum_d(ss);
+        for (int i = 0; i < 16; ++i) sq[i & 3] = __fma_rn((double)f[i], (double)f[i], sq[i & 3]);
+        double ss = warp_sum_d(__dadd_rn(__dadd_rn(sq[0], sq[1]), __dadd_rn(sq[2], sq[3])));
         if (lane == 0) redd[wt] = ss;
         bar_sync_n(bar, 32 * nw);
-        ss = warp_sum_d(lane < nw ? redd[lane] : 0.0);
-        const double r = __ddiv_rn(1.0, __dsqrt_rn(__dadd_rn(__ddiv_rn(ss, (double)K), (double)p.rms_eps)));
+        ss = lane < nw ? redd[lane] : 0.0;
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) ss = __dadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, off));
+        ss = __shfl_sync(0xffffffffu, ss, 0);
+        // within 2 units of fp64 of 1 / sqrt(ss / K + eps)
+        const double r = rsqrt(__fma_rn(ss, 1.0 / (double)K, (double)p.rms_eps));
 #pragma unroll
         for (int i = 0; i < 16; ++i) f[i] = __double2float_rn(__dmul_rn((double)f[i], r));
     }
@@ -257,8 +262,8 @@ __device__ __forceinline__ uint32_t moe_key(float v) {
 __device__ __forceinline__ bool moe_grid_sync(unsigned *counter, unsigned n, int *flag) {
     __syncthreads();
     if (threadIdx.x == 0) {
-        __threadfence();
-        atomicAdd(counter, 1u);
+        // release: what this CTA's threads wrote before the barrier above included
+        asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(counter) : "memory");
         const unsigned want = n * gridDim.x;
         int ok = 0;
         for (int i = 0; i < (1 << 20); ++i) {
@@ -271,7 +276,6 @@ __device__ __forceinline__ bool moe_grid_sync(unsigned *counter, unsigned n, int
         }
         if (!ok) flag_timeout();
         *flag = ok;
-        __threadfence();
     }
     __syncthreads();
     return *flag != 0;
@@ -340,158 +344,212 @@ struct MoeShared {
     MoeRed red;
 };
 
-// The strips [strip0, strip1) of one problem.  GATE: rows n0 .. n0 + 15 of gate and
-// up, activation to a.h; else rows n0 .. n0 + 31 of down, output to a.out.  Teams of
-// ks warps share a strip's column steps.  PD: steps in the ring.
-template <bool GATE, bool CONV, int PD>
-__device__ __forceinline__ void moe_strips(const MoeArgs &a, const MoeShared &sm, const MoeProblem &pb, int strip0, int strip1,
-                                           uint32_t x_s, uint32_t ring_s, int *red, int ks) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int team = warp / ks, kw = warp % ks, T = kMoeWarps / ks;
-    const int g = lane >> 2, t = lane & 3;
-    const int K = GATE ? a.D : a.F, N = GATE ? a.F : a.D, KB = K / 4, nsteps = KB / 64;
-    const int mine = (nsteps - kw + ks - 1) / ks, padded = (mine + PD - 1) / PD * PD;  // this warp's steps of a strip
-    const int64_t base = (int64_t)pb.expert * N * KB + (int64_t)g * KB + 16 * t + 64 * kw;
-    const uint32_t ring = ring_s + (uint32_t)(warp * PD * 2048 + 16 * lane);
-    auto load = [&](int slot, int strip, int i) {  // step i of this warp's
-        const uint8_t *p = (GATE ? a.gate : a.down) + base + (int64_t)strip * ((GATE ? 16 : 32) * KB) + 64 * ks * i;
-        const uint8_t *q = GATE ? a.up + (p - a.gate) : p + 16 * KB;
-        const uint32_t dst = ring + (uint32_t)(slot * 2048);
-        cp_async16(dst, p);
-        cp_async16(dst + 512, p + 8 * KB);
-        cp_async16(dst + 1024, q);
-        cp_async16(dst + 1536, q + 8 * KB);
-    };
-    // one group for the tokens' codes, one per step
-    const int XS = gemv_x_stride(K), cpr = K >> 4;
+// This CTA's share of a contraction phase: a run of consecutive strips of all
+// problems' strips.  GATE: a strip is rows n0 .. n0 + 15 of gate and up, giving
+// activations; else rows n0 .. n0 + 31 of down, giving outputs.  Teams of ks warps
+// share a strip's column steps, as many as keep every warp busy when runs are short.
+struct MoeRun {
+    int64_t s0, s1;
+    int ks;
+};
+
+template <bool GATE>
+__device__ __forceinline__ MoeRun moe_run(const MoeArgs &a, const MoeShared &sm) {
+    const int64_t total = (int64_t)sm.nprob * (GATE ? a.F / 16 : a.D / 32);
+    MoeRun r;
+    r.s0 = total * blockIdx.x / gridDim.x;
+    r.s1 = total * (blockIdx.x + 1) / gridDim.x;
+    const int run = (int)((total + gridDim.x - 1) / gridDim.x), steps = (GATE ? a.D : a.F) / 256;
+    r.ks = kMoeWarps;
+    while (r.ks > 1 && (kMoeWarps / r.ks < run || r.ks > steps)) r.ks >>= 1;
+    return r;
+}
+
+// Copies step i (of this warp's) of a strip to a slot of the warp's ring.
+template <bool GATE, int PD>
+__device__ __forceinline__ void moe_load(const MoeArgs &a, int expert, int strip, int kw, int ks, int i, uint32_t ring, int slot) {
+    const int lane = threadIdx.x & 31, N = GATE ? a.F : a.D, KB = (GATE ? a.D : a.F) / 4;
+    const int64_t off = ((int64_t)expert * N + strip * (GATE ? 16 : 32) + (lane >> 2)) * KB + 16 * (lane & 3) + 64 * (kw + ks * i);
+    const uint8_t *p = (GATE ? a.gate : a.down) + off, *q = GATE ? a.up + off : p + 16 * KB;
+    const uint32_t dst = ring + (uint32_t)(slot * 2048);
+    cp_async16(dst, p);
+    cp_async16(dst + 512, p + 8 * KB);
+    cp_async16(dst + 1024, q);
+    cp_async16(dst + 1536, q + 8 * KB);
+}
+
+// The first PD steps of this warp's run, one group each.
+template <bool GATE, int PD>
+__device__ __forceinline__ void moe_prime(const MoeArgs &a, const MoeShared &sm, const MoeRun &r, uint32_t ring) {
+    const int warp = threadIdx.x >> 5, team = warp / r.ks, kw = warp % r.ks;
+    const int spp = GATE ? a.F / 16 : a.D / 32, mine = ((GATE ? a.D : a.F) / 256 - kw + r.ks - 1) / r.ks;
+    const int q = r.s0 < r.s1 ? (int)(r.s0 / spp) : 0;
+    const int64_t first = (int64_t)q * spp, end = r.s1 < first + spp ? r.s1 : first + spp;
+    const int64_t s = r.s0 + team;
+#pragma unroll
+    for (int p = 0; p < PD; ++p) {
+        if (s < end && p < mine) moe_load<GATE, PD>(a, sm.prob[q].expert, (int)(s - first), kw, r.ks, p, ring, p);
+        cp_async_commit();
+    }
+}
+
+// A problem's token codes into shared memory (not committed).
+template <bool GATE>
+__device__ __forceinline__ void moe_stage(const MoeArgs &a, const MoeShared &sm, const MoeProblem &pb, uint32_t x_s) {
+    const int K = GATE ? a.D : a.F, XS = gemv_x_stride(K), cpr = K >> 4;
     for (int i = threadIdx.x; i < pb.count * cpr; i += kMoeThreads) {
         const int r = i / cpr, c = i - r * cpr;
         const int p = sm.sorted[pb.start + r];
         cp_async16(x_s + (uint32_t)(r * XS + 16 * c), (GATE ? a.xq + (int64_t)(p / a.k) * K : a.hq + (int64_t)p * K) + 16 * c);
     }
-    cp_async_commit();
-    int s = strip0 + team;
-#pragma unroll
-    for (int p = 0; p < PD; ++p) {
-        if (s < strip1 && p < mine) load(p, s, p);
-        cp_async_commit();
-    }
-    // this lane's tokens of a fragment: 2 t and 2 t + 1
-    float sv[2];
-    int rv[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int i = 2 * t + e < pb.count ? 2 * t + e : 0;
-        const int p = sm.sorted[pb.start + i], src = GATE ? p / a.k : p;
-        sv[e] = __ldcg((GATE ? a.sx : a.sh) + src);
-        rv[e] = __ldcg((GATE ? a.rs : a.rh) + src);
-    }
-    cp_async_wait_groups<PD>();
-    __syncthreads();
-    // token g of the problem (past the last: sums that are not used)
-    const uint32_t xr = x_s + (uint32_t)((g < pb.count ? g : pb.count - 1) * XS + 64 * t + 256 * kw);
-    const uint32_t xsw = (uint32_t)(t & 2) << 4;
-    int par = 0;
-    for (; s < strip1; s += T) {
-        int d[4][2][4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) d[j][0][i] = d[j][1][i] = 0;
-        for (int i0 = 0; i0 < padded; i0 += PD) {
-#pragma unroll
-            for (int p = 0; p < PD; ++p) {
-                const int i = i0 + p;
-                cp_async_wait_groups<PD - 1>();
-                if (i < mine) moe_step_mma<CONV>(d, ring + (uint32_t)(p * 2048), xr + (uint32_t)(256 * ks * i), xsw, a.enc);
-                // the step PD ahead: of this strip, or of this team's next
-                if (i + PD < padded) {
-                    if (i + PD < mine) load(p, s, i + PD);
-                } else if (s + T < strip1 && p < mine) {
-                    load(p, s + T, p);
-                }
-                cp_async_commit();
-            }
-        }
-        int acc[2][4];
-#pragma unroll
-        for (int mat = 0; mat < 2; ++mat)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)  // exact: d[j] is a multiple of 4^j
-                acc[mat][i] = d[0][mat][i] + (d[1][mat][i] >> 2) + (d[2][mat][i] >> 4) + (d[3][mat][i] >> 6);
-        int *slots = red + par * (kMoeWarps * kMoeSlot);
-        if (ks > 1) {
-            if (kw != 0) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) slots[warp * kMoeSlot + i * 32 + lane] = acc[i >> 2][i & 3];
-            }
-            bar_sync_n(1 + team, 32 * ks);
-            if (kw == 0) {
-                for (int w2 = warp + 1; w2 < warp + ks; ++w2)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] += slots[w2 * kMoeSlot + i * 32 + lane];
-            }
-            par ^= 1;
-        }
-        if (kw != 0) continue;
-        // The projections' values pass through this warp's own slot, so that the
-        // lanes share what follows evenly and stores cover whole rows' stretches:
-        // value (mat, row, token) at [mat][token / 2][(16 (token % 2) + row + 8 (token / 2)) % 32].
-        const int n0 = s * (GATE ? 16 : 32);
-        const float *g1 = GATE ? a.gate_gamma : a.down_gamma, *g2 = GATE ? a.up_gamma : a.down_gamma + (a.per_row ? 16 : 0);
-        float *val = reinterpret_cast<float *>(slots + warp * kMoeSlot);
-        __syncwarp();  // the slot's last readers are done
-#pragma unroll
-        for (int hi = 0; hi < 2; ++hi) {
-            const int64_t n = a.per_row ? (int64_t)pb.expert * N + n0 + g + 8 * hi : pb.expert;
-            const float ga = __ldg(g1 + n), gb = __ldg(g2 + n);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int c = 2 * hi + e, at = 32 * t + ((16 * e + g + 8 * hi + 8 * t) & 31);
-                val[at] = __fmul_rn(__int2float_rn(acc[0][c] - rv[e]), __fmul_rn(ga, sv[e]));
-                val[128 + at] = __fmul_rn(__int2float_rn(acc[1][c] - rv[e]), __fmul_rn(gb, sv[e]));
-            }
-        }
-        __syncwarp();
-        if (GATE) {
-            for (int i = lane; i < 16 * pb.count; i += 32) {
-                const int tok = i >> 4, row = i & 15, h = tok >> 1;
-                const int at = 32 * h + ((16 * (tok & 1) + row + 8 * h) & 31);
-                a.h[(int64_t)sm.sorted[pb.start + tok] * N + n0 + row] = moe_act(val[at], val[128 + at], a.clamp_val);
-            }
-        } else {
-            for (int tok = 0; tok < pb.count; ++tok) {
-                const int h = tok >> 1, at = 32 * h + ((16 * (tok & 1) + (lane & 15) + 8 * h) & 31);
-                a.out[(int64_t)sm.sorted[pb.start + tok] * N + n0 + lane] = val[128 * (lane >> 4) + at];
-            }
-        }
-    }
 }
 
-// One contraction phase over all problems: this CTA's run of strips.
+// The run, its first steps requested before (moe_prime).  While a problem's strips
+// are contracted, the next one's codes are copied to the other buffer, and its
+// first steps follow the last of this one in the ring.
 template <bool GATE, bool CONV, int PD>
-__device__ __forceinline__ void moe_contract(const MoeArgs &a, MoeShared &sm, uint8_t *dyn) {
-    const int K = GATE ? a.D : a.F, N = GATE ? a.F : a.D;
-    const int spp = N / (GATE ? 16 : 32);
-    const int64_t total = (int64_t)sm.nprob * spp;
-    const int64_t s0 = total * blockIdx.x / gridDim.x, s1 = total * (blockIdx.x + 1) / gridDim.x;
-    const int run = (int)((total + gridDim.x - 1) / gridDim.x);
-    // warps per strip: as many as keep every warp busy when runs are short
-    int ks = kMoeWarps;
-    while (ks > 1 && (kMoeWarps / ks < run || ks > K / 256)) ks >>= 1;
-    int *red = reinterpret_cast<int *>(dyn);
-    const uint32_t ring_s = smem_u32(dyn + kMoeRedBytes), x_s = ring_s + kMoeWarps * PD * 2048;
-    for (int64_t s = s0; s < s1;) {
-        const int q = (int)(s / spp);
-        const int64_t first = (int64_t)q * spp, end = s1 < first + spp ? s1 : first + spp;
-        __syncthreads();  // the previous problem's tokens and slots have been read
-        moe_strips<GATE, CONV, PD>(a, sm, sm.prob[q], (int)(s - first), (int)(end - first), x_s, ring_s, red, ks);
-        s = end;
-    }
+__device__ __forceinline__ void moe_contract(const MoeArgs &a, const MoeShared &sm, const MoeRun &run, uint32_t ring,
+                                             uint32_t x_s, int *red) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int ks = run.ks, team = warp / ks, kw = warp % ks, T = kMoeWarps / ks;
+    const int g = lane >> 2, t = lane & 3;
+    const int K = GATE ? a.D : a.F, N = GATE ? a.F : a.D, XS = gemv_x_stride(K);
+    const int spp = N / (GATE ? 16 : 32), nsteps = K / 256;
+    const int mine = (nsteps - kw + ks - 1) / ks, padded = (mine + PD - 1) / PD * PD;  // this warp's steps of a strip
+    const uint32_t xsw = (uint32_t)(t & 2) << 4;
+    float *val = reinterpret_cast<float *>(red + warp * kMoeSlot);
+    if (run.s0 >= run.s1) return;
+    int buf = 0;
+    moe_stage<GATE>(a, sm, sm.prob[run.s0 / spp], x_s);
+    cp_async_commit();
     cp_async_wait_groups<0>();
+    __syncthreads();
+    for (int64_t at = run.s0; at < run.s1;) {
+        const int q = (int)(at / spp);
+        const int64_t first = (int64_t)q * spp, end = run.s1 < first + spp ? run.s1 : first + spp;
+        const MoeProblem pb = sm.prob[q];
+        const bool more = end < run.s1;
+        const int next_expert = more ? sm.prob[q + 1].expert : 0;
+        const int next_strips = more ? (int)(run.s1 - end < spp ? run.s1 - end : spp) : 0;
+        if (more) moe_stage<GATE>(a, sm, sm.prob[q + 1], x_s + (uint32_t)((buf ^ 1) * kMoeChunk * XS));
+        cp_async_commit();
+        // this lane's tokens of a fragment: 2 t and 2 t + 1
+        float sv[2];
+        int rv[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = 2 * t + e < pb.count ? 2 * t + e : 0;
+            const int p = sm.sorted[pb.start + i], src = GATE ? p / a.k : p;
+            sv[e] = __ldcg((GATE ? a.sx : a.sh) + src);
+            rv[e] = __ldcg((GATE ? a.rs : a.rh) + src);
+        }
+        // token g of the problem (past the last: sums that are not used)
+        const uint32_t xr = x_s + (uint32_t)((buf * kMoeChunk + (g < pb.count ? g : pb.count - 1)) * XS + 64 * t + 256 * kw);
+        const int strip1 = (int)(end - first);
+        int committed = 0;  // groups of steps since the next problem's codes
+        for (int s = (int)(at - first) + team; s < strip1; s += T) {
+            const int n0 = s * (GATE ? 16 : 32);
+            // the strip's gammas, wanted at its end
+            float ga[2], gb[2];
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
+                const int64_t n = a.per_row ? (int64_t)pb.expert * N + n0 + g + 8 * hi : pb.expert;
+                ga[hi] = __ldg((GATE ? a.gate_gamma : a.down_gamma) + n);
+                gb[hi] = __ldg(GATE ? a.up_gamma + n : a.down_gamma + n + (a.per_row ? 16 : 0));
+            }
+            int d[4][2][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) d[j][0][i] = d[j][1][i] = 0;
+            for (int i0 = 0; i0 < padded; i0 += PD) {
+#pragma unroll
+                for (int p = 0; p < PD; ++p) {
+                    const int i = i0 + p;
+                    cp_async_wait_groups<PD - 1>();
+                    if (i < mine) moe_step_mma<CONV>(d, ring + (uint32_t)(p * 2048), xr + (uint32_t)(256 * ks * i), xsw, a.enc);
+                    // the slot takes the step PD ahead: of this strip, of this team's next,
+                    // or of its first of the next problem
+                    if (i + PD < padded) {
+                        if (i + PD < mine) moe_load<GATE, PD>(a, pb.expert, s, kw, ks, i + PD, ring, p);
+                    } else if (p < mine) {
+                        if (s + T < strip1)
+                            moe_load<GATE, PD>(a, pb.expert, s + T, kw, ks, p, ring, p);
+                        else if (team < next_strips)
+                            moe_load<GATE, PD>(a, next_expert, team, kw, ks, p, ring, p);
+                    }
+                    cp_async_commit();
+                }
+            }
+            committed += padded;
+            int acc[2][4];
+#pragma unroll
+            for (int mat = 0; mat < 2; ++mat)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)  // exact: d[j] is a multiple of 4^j
+                    acc[mat][i] = d[0][mat][i] + (d[1][mat][i] >> 2) + (d[2][mat][i] >> 4) + (d[3][mat][i] >> 6);
+            if (ks > 1) {
+                if (kw != 0) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) red[warp * kMoeSlot + i * 32 + lane] = acc[i >> 2][i & 3];
+                }
+                bar_sync_n(1 + team, 32 * ks);
+                if (kw == 0) {
+                    for (int w2 = warp + 1; w2 < warp + ks; ++w2)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] += red[w2 * kMoeSlot + i * 32 + lane];
+                }
+                bar_sync_n(1 + team, 32 * ks);  // the slots are written again
+            }
+            if (kw != 0) continue;
+            // The projections' values pass through this warp's own slot, so that the
+            // lanes share what follows evenly and stores cover whole rows' stretches:
+            // value (mat, row, token) at [mat][token / 2][(16 (token % 2) + row + 8 (token / 2)) % 32].
+            __syncwarp();  // the slot's last readers are done
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int c = 2 * hi + e, to = 32 * t + ((16 * e + g + 8 * hi + 8 * t) & 31);
+                    val[to] = __fmul_rn(__int2float_rn(acc[0][c] - rv[e]), __fmul_rn(ga[hi], sv[e]));
+                    val[128 + to] = __fmul_rn(__int2float_rn(acc[1][c] - rv[e]), __fmul_rn(gb[hi], sv[e]));
+                }
+            __syncwarp();
+            if (GATE) {
+                for (int i = lane; i < 16 * pb.count; i += 32) {
+                    const int tok = i >> 4, row = i & 15, h = tok >> 1;
+                    const int from = 32 * h + ((16 * (tok & 1) + row + 8 * h) & 31);
+                    a.h[(int64_t)sm.sorted[pb.start + tok] * N + n0 + row] = moe_act(val[from], val[128 + from], a.clamp_val);
+                }
+            } else {
+                for (int tok = 0; tok < pb.count; ++tok) {
+                    const int h = tok >> 1, from = 32 * h + ((16 * (tok & 1) + (lane & 15) + 8 * h) & 31);
+                    a.out[(int64_t)sm.sorted[pb.start + tok] * N + n0 + lane] = val[128 * (lane >> 4) + from];
+                }
+            }
+        }
+        if (more) {
+            if (committed == 0 && team < next_strips) {  // no strip of this problem: its ring is empty
+#pragma unroll
+                for (int p = 0; p < PD; ++p) {
+                    if (p < mine) moe_load<GATE, PD>(a, next_expert, team, kw, ks, p, ring, p);
+                    cp_async_commit();
+                }
+                committed = PD;
+            }
+            // the next problem's codes are in: older than the last PD - 1 groups, if so many follow them
+            if (committed >= PD - 1)
+                cp_async_wait_groups<PD - 1>();
+            else
+                cp_async_wait_groups<0>();
+            __syncthreads();
+            buf ^= 1;
+        }
+        at = end;
+    }
 }
 
-// PD: column steps in each warp's ring (4, or 3 where longer token rows need the room).
+// PD: column steps in each warp's ring (4, or 2 where longer token rows need the room).
 template <bool CONV, int PD>
 __global__ void __launch_bounds__(kMoeThreads, 1) tq_moe_experts_kernel(const __grid_constant__ MoeArgs a) {
     extern __shared__ __align__(128) uint8_t dyn[];
@@ -499,16 +557,14 @@ __global__ void __launch_bounds__(kMoeThreads, 1) tq_moe_experts_kernel(const __
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int P = a.M * a.k;
 
+    unsigned phase = 0;  // grid barriers passed
+
     // ---------------- choice ----------------
-    for (int m = warp; m < a.M; m += kMoeWarps) {
-        if (!a.router) {
-            for (int j = lane; j < a.k; j += 32) {
-                const int id = __ldg(a.ids + m * a.k + j);
-                sm.ids[m * a.k + j] = id >= 0 && id < a.E ? id : -1;
-                sm.w[m * a.k + j] = __ldg(a.weights + m * a.k + j);
-            }
-            continue;
-        }
+    // Up to 16 tokens, a warp of every CTA for each; more, a CTA for each, and the
+    // others read its choice after a barrier.
+    const bool spread = a.router && a.M > kMoeWarps;
+    for (int m = spread ? (int)blockIdx.x : warp; m < a.M; m += spread ? (int)gridDim.x : kMoeWarps) {
+        if (!a.router || (spread && warp != 0)) break;
         constexpr int V = kMoeMaxExperts / 32;
         float l[V];
         uint32_t key[V];
@@ -566,12 +622,19 @@ __global__ void __launch_bounds__(kMoeThreads, 1) tq_moe_experts_kernel(const __
             const float w = __double2float_rn(__ddiv_rn(ex, den));
             sm.ids[m * a.k + lane] = my_id;
             sm.w[m * a.k + lane] = w;
-            if (blockIdx.x == 0) {
+            if (spread || blockIdx.x == 0) {
                 a.ids[m * a.k + lane] = my_id;
                 a.weights[m * a.k + lane] = w;
             }
         }
     }
+    if (spread && !moe_grid_sync(a.barrier, ++phase, &sm.flag)) return;
+    if (!a.router || spread)
+        for (int p = threadIdx.x; p < P; p += kMoeThreads) {
+            const int id = __ldcg(a.ids + p);
+            sm.ids[p] = id >= 0 && id < a.E ? id : -1;
+            sm.w[p] = __ldcg(a.weights + p);
+        }
     // Pairs by expert, in order (every CTA must come to the same grouping).  Warps
     // rank the pairs of 32 at a time among those of the same expert and count them;
     // a thread per expert turns its counts into offsets.
@@ -639,8 +702,17 @@ __global__ void __launch_bounds__(kMoeThreads, 1) tq_moe_experts_kernel(const __
     __syncthreads();
 
     // ---------------- gate, up, activation ----------------
-    moe_contract<true, CONV, PD>(a, sm, dyn);
-    if (!moe_grid_sync(a.barrier, 1, &sm.flag)) return;
+    int *red = reinterpret_cast<int *>(dyn);
+    const uint32_t rings = smem_u32(dyn + kMoeRedBytes), x_s = rings + kMoeWarps * PD * 2048;
+    const uint32_t ring = rings + (uint32_t)(warp * PD * 2048 + 16 * lane);
+    const MoeRun run_gate = moe_run<true>(a, sm), run_down = moe_run<false>(a, sm);
+    moe_prime<true, PD>(a, sm, run_gate, ring);
+    moe_contract<true, CONV, PD>(a, sm, run_gate, ring, x_s, red);
+    moe_prime<false, PD>(a, sm, run_down, ring);  // on their way during the rotation
+    if (!moe_grid_sync(a.barrier, ++phase, &sm.flag)) {
+        cp_async_wait_groups<0>();
+        return;
+    }
     // ---------------- rotation and codes of every pair ----------------
     {
         const int nw = a.F / 512, fit = kMoeWarps / nw, teams = fit < 15 ? fit : 15;  // named barriers 1 .. 15
@@ -656,10 +728,13 @@ __global__ void __launch_bounds__(kMoeThreads, 1) tq_moe_experts_kernel(const __
             }
         }
     }
-    if (!moe_grid_sync(a.barrier, 2, &sm.flag)) return;
+    if (!moe_grid_sync(a.barrier, ++phase, &sm.flag)) {
+        cp_async_wait_groups<0>();
+        return;
+    }
     // ---------------- down ----------------
-    moe_contract<false, CONV, PD>(a, sm, dyn);
-    if (!moe_grid_sync(a.barrier, 3, &sm.flag)) return;
+    moe_contract<false, CONV, PD>(a, sm, run_down, ring, x_s, red);
+    if (!moe_grid_sync(a.barrier, ++phase, &sm.flag)) return;
     // ---------------- sum over the slots ----------------
     const int nv = a.D / 4;
     for (int i = (int)blockIdx.x * kMoeThreads + (int)threadIdx.x; i < a.M * nv; i += (int)gridDim.x * kMoeThreads) {
