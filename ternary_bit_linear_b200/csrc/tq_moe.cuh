@@ -349,48 +349,61 @@ struct MoeShared {
 // activations; else rows n0 .. n0 + 31 of down, giving outputs.  Teams of ks warps
 // share a strip's column steps, as many as keep every warp busy when runs are short.
 struct MoeRun {
-    int64_t s0, s1;
-    int ks;
+    int s0, s1;
+    int ks, team, kw;  // warps per strip; this warp's team and place in it
+    int mine;          // its column steps kw, kw + ks, ... of a strip
+    int spp;           // strips per problem
+    // the next step to request: problem, strip, step; strips of that problem end at `end`
+    int q, strip, end, i;
 };
 
 template <bool GATE>
 __device__ __forceinline__ MoeRun moe_run(const MoeArgs &a, const MoeShared &sm) {
-    const int64_t total = (int64_t)sm.nprob * (GATE ? a.F / 16 : a.D / 32);
     MoeRun r;
-    r.s0 = total * blockIdx.x / gridDim.x;
-    r.s1 = total * (blockIdx.x + 1) / gridDim.x;
-    const int run = (int)((total + gridDim.x - 1) / gridDim.x), steps = (GATE ? a.D : a.F) / 256;
+    r.spp = GATE ? a.F / 16 : a.D / 32;
+    const int total = sm.nprob * r.spp;  // at most 384 x 512
+    const int n = (int)gridDim.x, b = (int)blockIdx.x, steps = (GATE ? a.D : a.F) / 256;
+    r.s0 = (int)((unsigned)(total * b) / (unsigned)n);
+    r.s1 = (int)((unsigned)(total * (b + 1)) / (unsigned)n);
+    const int run = (total + n - 1) / n;
     r.ks = kMoeWarps;
     while (r.ks > 1 && (kMoeWarps / r.ks < run || r.ks > steps)) r.ks >>= 1;
+    const int warp = threadIdx.x >> 5;
+    r.team = warp / r.ks;
+    r.kw = warp % r.ks;
+    r.mine = (steps - r.kw + r.ks - 1) / r.ks;
+    r.q = r.s0 / r.spp;
+    r.strip = r.s0 - r.q * r.spp + r.team;
+    r.end = min(r.s1 - r.q * r.spp, r.spp);
+    r.i = 0;
     return r;
 }
 
-// Copies step i (of this warp's) of a strip to a slot of the warp's ring.
-template <bool GATE, int PD>
-__device__ __forceinline__ void moe_load(const MoeArgs &a, int expert, int strip, int kw, int ks, int i, uint32_t ring, int slot) {
-    const int lane = threadIdx.x & 31, N = GATE ? a.F : a.D, KB = (GATE ? a.D : a.F) / 4;
-    const int64_t off = ((int64_t)expert * N + strip * (GATE ? 16 : 32) + (lane >> 2)) * KB + 16 * (lane & 3) + 64 * (kw + ks * i);
-    const uint8_t *p = (GATE ? a.gate : a.down) + off, *q = GATE ? a.up + off : p + 16 * KB;
-    const uint32_t dst = ring + (uint32_t)(slot * 2048);
-    cp_async16(dst, p);
-    cp_async16(dst + 512, p + 8 * KB);
-    cp_async16(dst + 1024, q);
-    cp_async16(dst + 1536, q + 8 * KB);
-}
-
-// The first PD steps of this warp's run, one group each.
-template <bool GATE, int PD>
-__device__ __forceinline__ void moe_prime(const MoeArgs &a, const MoeShared &sm, const MoeRun &r, uint32_t ring) {
-    const int warp = threadIdx.x >> 5, team = warp / r.ks, kw = warp % r.ks;
-    const int spp = GATE ? a.F / 16 : a.D / 32, mine = ((GATE ? a.D : a.F) / 256 - kw + r.ks - 1) / r.ks;
-    const int q = r.s0 < r.s1 ? (int)(r.s0 / spp) : 0;
-    const int64_t first = (int64_t)q * spp, end = r.s1 < first + spp ? r.s1 : first + spp;
-    const int64_t s = r.s0 + team;
-#pragma unroll
-    for (int p = 0; p < PD; ++p) {
-        if (s < end && p < mine) moe_load<GATE, PD>(a, sm.prob[q].expert, (int)(s - first), kw, r.ks, p, ring, p);
-        cp_async_commit();
+// Requests the next step of this warp's run into a slot of its ring: one group, an
+// empty one past the end.
+template <bool GATE>
+__device__ __forceinline__ void moe_load(const MoeArgs &a, const MoeShared &sm, MoeRun &r, uint32_t slot) {
+    while (r.strip >= r.end) {  // on to the next problem of the run
+        if ((r.q + 1) * r.spp >= r.s1) break;
+        ++r.q;
+        r.strip = r.team;
+        r.end = min(r.s1 - r.q * r.spp, r.spp);
     }
+    if (r.strip < r.end) {
+        const int lane = threadIdx.x & 31, N = GATE ? a.F : a.D, KB = (GATE ? a.D : a.F) / 4;
+        const int64_t off = ((int64_t)sm.prob[r.q].expert * N + r.strip * (GATE ? 16 : 32) + (lane >> 2)) * KB + 16 * (lane & 3) +
+                            64 * (r.kw + r.ks * r.i);
+        const uint8_t *p = (GATE ? a.gate : a.down) + off, *q = GATE ? a.up + off : p + 16 * KB;
+        cp_async16(slot, p);
+        cp_async16(slot + 512, p + 8 * KB);
+        cp_async16(slot + 1024, q);
+        cp_async16(slot + 1536, q + 8 * KB);
+        if (++r.i == r.mine) {
+            r.i = 0;
+            r.strip += kMoeWarps / r.ks;
+        }
+    }
+    cp_async_commit();
 }
 
 // A problem's token codes into shared memory (not committed).
@@ -404,18 +417,16 @@ __device__ __forceinline__ void moe_stage(const MoeArgs &a, const MoeShared &sm,
     }
 }
 
-// The run, its first steps requested before (moe_prime).  While a problem's strips
-// are contracted, the next one's codes are copied to the other buffer, and its
-// first steps follow the last of this one in the ring.
+// The run, the first PD steps of each warp requested before.  While a problem's
+// strips are contracted, the next one's codes are copied to the other buffer; the
+// ring goes on from strip to strip and problem to problem.
 template <bool GATE, bool CONV, int PD>
-__device__ __forceinline__ void moe_contract(const MoeArgs &a, const MoeShared &sm, const MoeRun &run, uint32_t ring,
-                                             uint32_t x_s, int *red) {
+__device__ __forceinline__ void moe_contract(const MoeArgs &a, const MoeShared &sm, MoeRun &run, uint32_t ring, uint32_t x_s,
+                                             int *red) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int ks = run.ks, team = warp / ks, kw = warp % ks, T = kMoeWarps / ks;
+    const int ks = run.ks, team = run.team, kw = run.kw, T = kMoeWarps / ks, spp = run.spp;
     const int g = lane >> 2, t = lane & 3;
     const int K = GATE ? a.D : a.F, N = GATE ? a.F : a.D, XS = gemv_x_stride(K);
-    const int spp = N / (GATE ? 16 : 32), nsteps = K / 256;
-    const int mine = (nsteps - kw + ks - 1) / ks, padded = (mine + PD - 1) / PD * PD;  // this warp's steps of a strip
     const uint32_t xsw = (uint32_t)(t & 2) << 4;
     float *val = reinterpret_cast<float *>(red + warp * kMoeSlot);
     if (run.s0 >= run.s1) return;
@@ -424,13 +435,11 @@ __device__ __forceinline__ void moe_contract(const MoeArgs &a, const MoeShared &
     cp_async_commit();
     cp_async_wait_groups<0>();
     __syncthreads();
-    for (int64_t at = run.s0; at < run.s1;) {
-        const int q = (int)(at / spp);
-        const int64_t first = (int64_t)q * spp, end = run.s1 < first + spp ? run.s1 : first + spp;
+    int slot = 0;
+    for (int at = run.s0, q = run.s0 / spp; at < run.s1; ++q) {
+        const int first = q * spp, end = min(run.s1, first + spp);
         const MoeProblem pb = sm.prob[q];
         const bool more = end < run.s1;
-        const int next_expert = more ? sm.prob[q + 1].expert : 0;
-        const int next_strips = more ? (int)(run.s1 - end < spp ? run.s1 - end : spp) : 0;
         if (more) moe_stage<GATE>(a, sm, sm.prob[q + 1], x_s + (uint32_t)((buf ^ 1) * kMoeChunk * XS));
         cp_async_commit();
         // this lane's tokens of a fragment: 2 t and 2 t + 1
@@ -445,9 +454,8 @@ __device__ __forceinline__ void moe_contract(const MoeArgs &a, const MoeShared &
         }
         // token g of the problem (past the last: sums that are not used)
         const uint32_t xr = x_s + (uint32_t)((buf * kMoeChunk + (g < pb.count ? g : pb.count - 1)) * XS + 64 * t + 256 * kw);
-        const int strip1 = (int)(end - first);
         int committed = 0;  // groups of steps since the next problem's codes
-        for (int s = (int)(at - first) + team; s < strip1; s += T) {
+        for (int s = at - first + team; s < end - first; s += T) {
             const int n0 = s * (GATE ? 16 : 32);
             // the strip's gammas, wanted at its end
             float ga[2], gb[2];
@@ -462,26 +470,15 @@ __device__ __forceinline__ void moe_contract(const MoeArgs &a, const MoeShared &
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) d[j][0][i] = d[j][1][i] = 0;
-            for (int i0 = 0; i0 < padded; i0 += PD) {
-#pragma unroll
-                for (int p = 0; p < PD; ++p) {
-                    const int i = i0 + p;
-                    cp_async_wait_groups<PD - 1>();
-                    if (i < mine) moe_step_mma<CONV>(d, ring + (uint32_t)(p * 2048), xr + (uint32_t)(256 * ks * i), xsw, a.enc);
-                    // the slot takes the step PD ahead: of this strip, of this team's next,
-                    // or of its first of the next problem
-                    if (i + PD < padded) {
-                        if (i + PD < mine) moe_load<GATE, PD>(a, pb.expert, s, kw, ks, i + PD, ring, p);
-                    } else if (p < mine) {
-                        if (s + T < strip1)
-                            moe_load<GATE, PD>(a, pb.expert, s + T, kw, ks, p, ring, p);
-                        else if (team < next_strips)
-                            moe_load<GATE, PD>(a, next_expert, team, kw, ks, p, ring, p);
-                    }
-                    cp_async_commit();
-                }
+#pragma unroll 1
+            for (int i = 0; i < run.mine; ++i) {
+                cp_async_wait_groups<PD - 1>();
+                const uint32_t from = ring + (uint32_t)(slot * 2048);
+                moe_step_mma<CONV>(d, from, xr + (uint32_t)(256 * ks * i), xsw, a.enc);
+                moe_load<GATE>(a, sm, run, from);  // the slot takes the step PD ahead
+                slot = slot + 1 == PD ? 0 : slot + 1;
             }
-            committed += padded;
+            committed += run.mine;
             int acc[2][4];
 #pragma unroll
             for (int mat = 0; mat < 2; ++mat)
@@ -529,14 +526,6 @@ __device__ __forceinline__ void moe_contract(const MoeArgs &a, const MoeShared &
             }
         }
         if (more) {
-            if (committed == 0 && team < next_strips) {  // no strip of this problem: its ring is empty
-#pragma unroll
-                for (int p = 0; p < PD; ++p) {
-                    if (p < mine) moe_load<GATE, PD>(a, next_expert, team, kw, ks, p, ring, p);
-                    cp_async_commit();
-                }
-                committed = PD;
-            }
             // the next problem's codes are in: older than the last PD - 1 groups, if so many follow them
             if (committed >= PD - 1)
                 cp_async_wait_groups<PD - 1>();
@@ -705,10 +694,13 @@ __global__ void __launch_bounds__(kMoeThreads, 1) tq_moe_experts_kernel(const __
     int *red = reinterpret_cast<int *>(dyn);
     const uint32_t rings = smem_u32(dyn + kMoeRedBytes), x_s = rings + kMoeWarps * PD * 2048;
     const uint32_t ring = rings + (uint32_t)(warp * PD * 2048 + 16 * lane);
-    const MoeRun run_gate = moe_run<true>(a, sm), run_down = moe_run<false>(a, sm);
-    moe_prime<true, PD>(a, sm, run_gate, ring);
-    moe_contract<true, CONV, PD>(a, sm, run_gate, ring, x_s, red);
-    moe_prime<false, PD>(a, sm, run_down, ring);  // on their way during the rotation
+    {
+        MoeRun run = moe_run<true>(a, sm);
+        for (int p = 0; p < PD; ++p) moe_load<true>(a, sm, run, ring + 2048u * p);
+        moe_contract<true, CONV, PD>(a, sm, run, ring, x_s, red);
+    }
+    MoeRun run = moe_run<false>(a, sm);
+    for (int p = 0; p < PD; ++p) moe_load<false>(a, sm, run, ring + 2048u * p);  // on their way during the rotation
     if (!moe_grid_sync(a.barrier, ++phase, &sm.flag)) {
         cp_async_wait_groups<0>();
         return;
@@ -733,7 +725,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) tq_moe_experts_kernel(const __
         return;
     }
     // ---------------- down ----------------
-    moe_contract<false, CONV, PD>(a, sm, run_down, ring, x_s, red);
+    moe_contract<false, CONV, PD>(a, sm, run, ring, x_s, red);
     if (!moe_grid_sync(a.barrier, ++phase, &sm.flag)) return;
     // ---------------- sum over the slots ----------------
     const int nv = a.D / 4;
