@@ -592,17 +592,17 @@ def quantize_fp8(x, square: bool = False, transpose: bool = False, rmsnorm: bool
     import torch
 
     R, C = x.shape
-    rb, cb = -(-R // 128), -(-C // 128)
-    flags = ((FLAG_FP8_SQUARE if square else 0) | (FLAG_RMSNORM if rmsnorm else 0) |
-             (FLAG_BF16_INPUT if x.dtype is torch.bfloat16 else 0))
-    f8, f32 = torch.float8_e4m3fn, torch.float32
-    q, s = x.new_empty((R, fp8_row_bytes(C)), dtype=f8), x.new_empty((rb, cb) if square else (cb, R), dtype=f32)
-    if not transpose:
-        quantize_fp8_(x, flags, q, s, None, None, rms_gain, rms_eps, stream)
-        return q, s
-    qt, st = x.new_empty((C, fp8_row_bytes(R)), dtype=f8), x.new_empty((cb, rb) if square else (rb, C), dtype=f32)
-    quantize_fp8_(x, flags, q, s, qt, st, rms_gain, rms_eps, stream)
-    return q, s, qt, st
+    rb, cb, ldq, ldt = (R + 127) // 128, (C + 127) // 128, (C + 15) // 16 * 16, (R + 15) // 16 * 16
+    dev, f8, f32, bf16 = x.device, torch.float8_e4m3fn, torch.float32, x.dtype is torch.bfloat16
+    flags = ((FLAG_FP8_SQUARE if square else 0) | (FLAG_RMSNORM if rmsnorm else 0) | (FLAG_BF16_INPUT if bf16 else 0))
+    q, s = x.new_empty((R, ldq), dtype=f8), x.new_empty((rb, cb) if square else (cb, R), dtype=f32)
+    qt = st = None
+    if transpose:
+        qt, st = x.new_empty((C, ldt), dtype=f8), x.new_empty((cb, rb) if square else (rb, C), dtype=f32)
+    _call("tq_quantize_fp8", dev, stream, _fit(x, torch.bfloat16 if bf16 else f32, (R, C), dev, "x"), R, C, flags,
+          None if rms_gain is None else _fit(rms_gain, f32, (C,), dev, "rms_gain"), rms_eps, q.data_ptr(), s.data_ptr(),
+          qt.data_ptr() if transpose else None, st.data_ptr() if transpose else None)
+    return (q, s, qt, st) if transpose else (q, s)
 
 
 def fp8_gemm(xq, s_x, wq, s_w, K: int, w_rows: bool = False, bf16: bool = False, stream=None):

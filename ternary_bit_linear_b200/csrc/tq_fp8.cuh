@@ -26,17 +26,48 @@ constexpr float kFp8Floor = 1e-20f;
 
 __device__ __forceinline__ float fp8_scale(float amax) { return __fdiv_rn(fmaxf(amax, kFp8Floor), kFp8Max); }
 
-// Codes of x / s for four elements, lowest address first; s per element, or one.
-__device__ __forceinline__ uint32_t fp8_codes4(float4 v, float4 s) {
+// A block's scale and its correctly rounded reciprocal.
+struct Fp8Scale {
+    float s, inv;
+};
+__device__ __forceinline__ Fp8Scale fp8_block_scale(float amax) {
+    const float s = fp8_scale(amax);
+    return Fp8Scale{s, __frcp_rn(s)};
+}
+
+// fp32(v / s) from the reciprocal: Markstein, "Computation of elementary functions on
+// the IBM RISC System/6000 processor" (1990): a quotient within one unit, here v inv
+// corrected once, becomes the correctly rounded one by its exact remainder times
+// the correctly rounded reciprocal.  The remainders of quotients near a rounding
+// border of e4m3 are normal numbers (the floor of s).  An infinite s has inv = 0,
+// and v * 0 is what v / s would be.
+__device__ __forceinline__ float fp8_quotient(float v, Fp8Scale k) {
+    const float q0 = __fmul_rn(v, k.inv);
+    const float q1 = __fmaf_rn(__fmaf_rn(-q0, k.s, v), k.inv, q0);
+    const float q2 = __fmaf_rn(__fmaf_rn(-q1, k.s, v), k.inv, q1);
+    return k.inv == 0.0f ? q0 : q2;
+}
+
+// Codes of four quotients, lowest address first.
+__device__ __forceinline__ uint32_t fp8_pack4(float x, float y, float z, float w) {
     uint16_t lo, hi;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(__fdiv_rn(v.y, s.y)), "f"(__fdiv_rn(v.x, s.x)));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(__fdiv_rn(v.w, s.w)), "f"(__fdiv_rn(v.z, s.z)));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y), "f"(x));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(w), "f"(z));
     return (uint32_t)lo | ((uint32_t)hi << 16);
 }
-__device__ __forceinline__ uint32_t fp8_codes4(float4 v, float s) { return fp8_codes4(v, make_float4(s, s, s, s)); }
+__device__ __forceinline__ uint32_t fp8_codes4(float4 v, Fp8Scale k) {
+    return fp8_pack4(fp8_quotient(v.x, k), fp8_quotient(v.y, k), fp8_quotient(v.z, k), fp8_quotient(v.w, k));
+}
 
 __device__ __forceinline__ float abs_max4(float4 v) {
     return fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+}
+
+// One step of a reduction of several maxima at once: a lane keeps the second of
+// two (`up`) or the first, joined with its partner's of the same.
+__device__ __forceinline__ void fp8_halve(float &first, float second, bool up, int off) {
+    const float give = up ? first : second, keep = up ? second : first;
+    first = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, off));
 }
 
 // Four elements at column c (c % 4 == 0) of a row of C elements; zeros past the
@@ -84,12 +115,23 @@ __global__ void __launch_bounds__(32 * kFp8RowWarps)
     float4 v[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = fp8_load4<BF16, VEC>(x, row, C, c0 + 128 * j);
+    // the four maxima by halving exchanges: block lane / 8's ends up in every lane
+    float m[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m[j] = abs_max4(v[j]);
+    fp8_halve(m[0], m[2], lane & 16, 16);
+    fp8_halve(m[1], m[3], lane & 16, 16);
+    fp8_halve(m[0], m[1], lane & 8, 8);
+#pragma unroll
+    for (int off = 4; off > 0; off >>= 1) m[0] = fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], off));
+    const Fp8Scale mine = fp8_block_scale(m[0]);
+    const int64_t b = (c0 - 4 * lane) / 128 + (lane >> 3);
+    if (!(lane & 7) && b * 128 < C) s[b * R + row] = mine.s;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const float sc = fp8_scale(warp_max(abs_max4(v[j])));
+        const Fp8Scale sc{__shfl_sync(0xffffffffu, mine.s, 8 * j), __shfl_sync(0xffffffffu, mine.inv, 8 * j)};
         const int64_t c = c0 + 128 * j;
         if (c < ldq) *reinterpret_cast<uint32_t *>(q + row * ldq + c) = fp8_codes4(v[j], sc);
-        if (lane == 0 && c < C) s[(c >> 7) * R + row] = sc;
     }
 }
 
@@ -126,9 +168,9 @@ __global__ void __launch_bounds__(kActThreads)
             e[i] = __double2float_rn(__dmul_rn(__dmul_rn((double)e[i], r), g));
         }
         v = make_float4(e[0], e[1], e[2], e[3]);
-        const float sc = fp8_scale(warp_max(abs_max4(v)));
+        const Fp8Scale sc = fp8_block_scale(warp_max(abs_max4(v)));
         if (c < ldq) *reinterpret_cast<uint32_t *>(q + row * ldq + c) = fp8_codes4(v, sc);
-        if (lane == 0) s[(b >> 7) * R + row] = sc;
+        if (lane == 0) s[(b >> 7) * R + row] = sc.s;
     }
 }
 
@@ -142,7 +184,7 @@ __global__ void __launch_bounds__(kActThreads)
 // memory to leave in whole 128-byte rows.
 // ---------------------------------------------------------------------------
 template <bool BF16, bool VEC, bool SQUARE, bool TRANS>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 3)
     tq_fp8_tile_kernel(const void *__restrict__ x, int64_t R, int64_t C, int64_t ldq, int64_t ldt,
                        uint8_t *__restrict__ q, float *__restrict__ s, uint8_t *__restrict__ qt,
                        float *__restrict__ st) {
@@ -159,7 +201,7 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
         for (int i = 0; i < 16; ++i)
             v[i] = r0 + i < R ? fp8_load4<BF16, VEC>(x, r0 + i, C, c) : make_float4(0.f, 0.f, 0.f, 0.f);
-        float sq = 0.0f;
+        Fp8Scale sq{0.0f, 0.0f};
         if (SQUARE) {
             float m = 0.0f;
 #pragma unroll
@@ -167,10 +209,10 @@ __global__ void __launch_bounds__(256)
             m = warp_max(m);
             if (lane == 0) red[0][warp] = m;
             __syncthreads();
-            sq = fp8_scale(warp_max(red[0][lane & 7]));
+            sq = fp8_block_scale(warp_max(red[0][lane & 7]));
             if (threadIdx.x == 0) {
-                s[rb * CB + cb] = sq;
-                if (TRANS) st[cb * ((R + 127) >> 7) + rb] = sq;
+                s[rb * CB + cb] = sq.s;
+                if (TRANS) st[cb * ((R + 127) >> 7) + rb] = sq.s;
             }
         } else if (TRANS) {
             float4 m = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -183,16 +225,31 @@ __global__ void __launch_bounds__(256)
             }
             *reinterpret_cast<float4 *>(&red[warp][4 * lane]) = m;
         }
+        // A row's maximum over the 32 lanes: halving exchanges leave row lane / 2's in
+        // every lane (31 shuffles, not 80), which makes that row's scale for all.
+        Fp8Scale mine{0.0f, 0.0f};
+        if (!SQUARE) {
+            float m[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) m[i] = abs_max4(v[i]);
+#pragma unroll
+            for (int n = 8; n >= 1; n >>= 1) {
+                const bool up = lane & (2 * n);
+#pragma unroll
+                for (int i = 0; i < n; ++i) fp8_halve(m[i], m[i + n], up, 2 * n);
+            }
+            mine = fp8_block_scale(fmaxf(m[0], __shfl_xor_sync(0xffffffffu, m[0], 1)));
+            if (!(lane & 1) && r0 + (lane >> 1) < R) s[cb * R + r0 + (lane >> 1)] = mine.s;
+        }
         // codes in x's own order
         uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const float sc = SQUARE ? sq : fp8_scale(warp_max(abs_max4(v[i])));
+            const Fp8Scale sc = SQUARE ? sq
+                                       : Fp8Scale{__shfl_sync(0xffffffffu, mine.s, 2 * i),
+                                                  __shfl_sync(0xffffffffu, mine.inv, 2 * i)};
             w[i] = fp8_codes4(v[i], sc);
-            if (r0 + i < R) {
-                if (c < ldq) *reinterpret_cast<uint32_t *>(q + (r0 + i) * ldq + c) = w[i];
-                if (!SQUARE && lane == 0) s[cb * R + r0 + i] = sc;
-            }
+            if (r0 + i < R && c < ldq) *reinterpret_cast<uint32_t *>(q + (r0 + i) * ldq + c) = w[i];
         }
         if (TRANS) {
             if (!SQUARE) {  // the columns' own scales and codes
@@ -203,16 +260,16 @@ __global__ void __launch_bounds__(256)
                     const float4 t = *reinterpret_cast<const float4 *>(&red[k][4 * lane]);
                     m = make_float4(fmaxf(m.x, t.x), fmaxf(m.y, t.y), fmaxf(m.z, t.z), fmaxf(m.w, t.w));
                 }
-                const float4 sc = make_float4(fp8_scale(m.x), fp8_scale(m.y), fp8_scale(m.z), fp8_scale(m.w));
+                const Fp8Scale k[4] = {fp8_block_scale(m.x), fp8_block_scale(m.y), fp8_block_scale(m.z), fp8_block_scale(m.w)};
                 if (warp == 0) {
-                    const float e[4] = {sc.x, sc.y, sc.z, sc.w};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (c + k < C) st[rb * C + c + k] = e[k];
+                    for (int e = 0; e < 4; ++e)
+                        if (c + e < C) st[rb * C + c + e] = k[e].s;
                 }
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    w[i] = fp8_codes4(v[i], sc);
+                    w[i] = fp8_pack4(fp8_quotient(v[i].x, k[0]), fp8_quotient(v[i].y, k[1]), fp8_quotient(v[i].z, k[2]),
+                                     fp8_quotient(v[i].w, k[3]));
             }
             // byte e of words 4k .. 4k + 3 -> word k of column e's 16 rows.  Chunk
             // (16 rows) w of column col sits at chunk w ^ (col / 4 % 8): a quarter
