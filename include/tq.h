@@ -404,7 +404,8 @@ TQ_API size_t tq_swiglu_workspace_bytes(int64_t M, int64_t d_model, int64_t d_ff
  *              same time need their own.
  *   flags      TQ_FLAG_FWHT (required), TQ_FLAG_RMSNORM, TQ_FLAG_NORM_TOPK (with a
  *              router only), TQ_GAMMA_PER_ROW, TQ_FLAG_SANITIZE_NONFINITE (of x, for
- *              the router too, and of the activations), TQ_FLAG_WEIGHTS_STATIC, TQ_ENC_*.
+ *              the router too, and of the activations), TQ_ENC_*, and TQ_FLAG_WEIGHTS_STATIC
+ *              (accepted; the call does not start before the previous work ends).
  * The second launch is a cooperative one, one block per SM whose blocks wait for
  * one another (each wait bounded): it starts when the whole GPU has room for it.
  */

@@ -399,8 +399,8 @@ def moe_swiglu_(x, router, gate, up, down, flags, y, ids, weights, workspace, cl
           _fit(up[0], u8, (E, F, D // 4), dev, "up packed"), _fit(up[1], f32, gf, dev, "up gamma"),
           _fit(down[0], u8, (E, D, F // 4), dev, "down packed"), _fit(down[1], f32, gd, dev, "down gamma"),
           _fit(y, f32, (M, D), dev, "y"), _fit(ids, torch.int32, (M, k), dev, "ids"),
-          _fit(weights, f32, (M, k), dev, "weights"), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
+          _fit(weights, f32, (M, k), dev, "weights"),
+          _fit(workspace, u8, (workspace.numel(),), dev, "workspace"), workspace.numel())
 
 
 def quantize_fp8_(x, flags, q, s, qt=None, st=None, rms_gain=None, rms_eps=1e-6, stream=None):

@@ -7,6 +7,10 @@ self-contained command that ncu captures are taken on.
 Training kernels: bwd (input gradient, dY [M][N] against the packed [N][K]),
 ste and flip (latent weights / gradient [N][K]).
 
+moe: a mixture-of-experts layer of --G experts, --topk of them per token (d_model K,
+d_ffn N).  fp8: block-scaled e4m3 product of M tokens with [N][K]; quant: its
+weight quantisation with the transpose.
+
 Inputs are random device tensors of the workloads' distributions (values do
 not affect timing); every call goes through the C ABI.  Exits non-zero if a
 call fails or the device status word reports a timeout.
@@ -24,11 +28,12 @@ def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--kernel", required=True,
                     choices=["pack_row", "pack_tensor", "act", "fwht", "gemv", "gemm", "grouped", "fused", "bwd", "ste",
-                             "flip"])
+                             "flip", "moe", "fp8", "quant"])
     ap.add_argument("--G", type=int, default=8, help="layers per grouped call")
     ap.add_argument("--M", type=int, default=8)
     ap.add_argument("--N", type=int, default=4096)
     ap.add_argument("--K", type=int, default=4096)
+    ap.add_argument("--topk", type=int, default=2, help="experts per token (moe)")
     ap.add_argument("--reps", type=int, default=3)
     ap.add_argument("--ready", action="store_true",
                     help="contractions with TQ_FLAG_INPUTS_READY (independent calls: the streaming GEMV)")
@@ -62,9 +67,28 @@ def main():
         G = torch.randn((N, K), generator=g, device=dev)
         GW = torch.empty_like(G)
         state = tq.seed(42)
+    if a.kernel == "moe":  # the same packed matrices for every expert's gate and up, their own for down
+        E, D, F = a.G, K, N
+        mfl = tq.FLAG_FWHT | tq.FLAG_RMSNORM | tq.GAMMA_PER_ROW | tq.FLAG_NORM_TOPK
+        stack = lambda p, s: (p.unsqueeze(0).repeat(E, 1, 1), s.unsqueeze(0).repeat(E, 1))  # noqa: E731
+        mgate, mup = stack(packed, gamma), stack(packed, gamma)
+        mdown = stack(*tq.quantize_ternary_pack(torch.randn((D, F), generator=g, device=dev) * 0.02, per_row=True))
+        router = torch.randn((E, D), generator=g, device=dev) * 0.05
+        my, mids = torch.empty_like(X), torch.empty((M, a.topk), dtype=torch.int32, device=dev)
+        mwt = torch.empty((M, a.topk), device=dev)
+        mws = torch.empty((tq.moe_workspace_bytes(M, D, F, E, a.topk, mfl),), dtype=torch.uint8, device=dev)
+    if a.kernel in ("fp8", "quant"):
+        x8, x8s = tq.quantize_fp8(X)
+        w8 = tq.quantize_fp8(W, square=True, transpose=True)
     torch.cuda.synchronize()
     for _ in range(a.reps):
-        if a.kernel in ("pack_row", "pack_tensor"):
+        if a.kernel == "moe":
+            tq.moe_swiglu_(X, router, mgate, mup, mdown, mfl, my, mids, mwt, mws)
+        elif a.kernel == "fp8":
+            tq.fp8_gemm_(x8, x8s, w8[0], w8[1], K, 0, y)
+        elif a.kernel == "quant":
+            tq.quantize_fp8_(W, tq.FLAG_FP8_SQUARE, *w8)
+        elif a.kernel in ("pack_row", "pack_tensor"):
             tq.quantize_ternary_pack_(W, flags, packed, gamma, pws)
         elif a.kernel == "act":
             tq.quantize_act_int8_(X, 0, 0.05, 40.0, xq, sx, rs)
