@@ -353,26 +353,27 @@ def fp8_row_bytes(K: int) -> int:
     return (K + 15) // 16 * 16
 
 
-def _fit(t, dtype, shape, device, name):
-    """The check of _need for calls that last a few microseconds."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {device}, got "
+def _fit(t, dtype, shape, dev, name):
+    """The check of _need for calls that last a few microseconds; `dev` is the index of
+    the CUDA device of all tensors of the call.  Returns the address."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on cuda:{dev}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
-def _call(fn, device, stream, *args):
-    """The C call on the tensors' device: on `stream`, or on that device's current stream."""
+def _call(fn, dev, stream, *args):
+    """The C call on device `dev`: on `stream`, or on that device's current stream."""
     import torch
 
-    if device.type != "cuda":
-        raise ValueError(f"{fn}: expected CUDA tensors, got {device}")
+    if dev < 0:
+        raise ValueError(f"{fn}: expected CUDA tensors")
     f = getattr(_lib or load(), fn)
-    s = torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
-    if device.index == torch._C._cuda_getDevice():
+    s = torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
         code = f(*args, s)
     else:
-        with torch.cuda.device(device):
+        with torch.cuda.device(dev):
             code = f(*args, s)
     if code != 0:
         raise TqError(fn, code)
@@ -391,7 +392,7 @@ def moe_swiglu_(x, router, gate, up, down, flags, y, ids, weights, workspace, cl
     M, D = x.shape
     E, F = gate[0].shape[0], gate[0].shape[1]
     k = ids.shape[1]
-    dev, f32, u8 = x.device, torch.float32, torch.uint8
+    dev, f32, u8 = x.get_device(), torch.float32, torch.uint8
     gf, gd = ((E, F), (E, D)) if flags & GAMMA_PER_ROW else ((E,), (E,))
     _call("tq_moe_swiglu", dev, stream, _fit(x, f32, (M, D), dev, "x"), M, D, F, E, k, flags, clamp_val,
           None if router is None else _fit(router, f32, (E, D), dev, "router"),
@@ -411,7 +412,7 @@ def quantize_fp8_(x, flags, q, s, qt=None, st=None, rms_gain=None, rms_eps=1e-6,
 
     R, C = x.shape
     rb, cb = -(-R // 128), -(-C // 128)
-    square, dev, f8, f32 = flags & FLAG_FP8_SQUARE, x.device, torch.float8_e4m3fn, torch.float32
+    square, dev, f8, f32 = flags & FLAG_FP8_SQUARE, x.get_device(), torch.float8_e4m3fn, torch.float32
     _call("tq_quantize_fp8", dev, stream,
           _fit(x, torch.bfloat16 if flags & FLAG_BF16_INPUT else f32, (R, C), dev, "x"), R, C, flags,
           None if rms_gain is None else _fit(rms_gain, f32, (C,), dev, "rms_gain"), rms_eps,
@@ -428,7 +429,7 @@ def fp8_gemm_(xq, s_x, wq, s_w, K, flags, y, stream=None):
     import torch
 
     M, N, ld, kb = xq.shape[0], wq.shape[0], (K + 15) // 16 * 16, -(-K // 128)
-    dev, f8, f32 = xq.device, torch.float8_e4m3fn, torch.float32
+    dev, f8, f32 = xq.get_device(), torch.float8_e4m3fn, torch.float32
     _call("tq_fp8_gemm", dev, stream, _fit(xq, f8, (M, ld), dev, "xq"), _fit(s_x, f32, (kb, M), dev, "s_x"),
           _fit(wq, f8, (N, ld), dev, "wq"),
           _fit(s_w, f32, (kb, N) if flags & FLAG_FP8_W_ROWS else (-(-N // 128), kb), dev, "s_w"), flags, M, N, K,
@@ -586,6 +587,13 @@ def moe_swiglu(x, router, gate, up, down, top_k: int, per_row: bool = False, rms
     return y, ids, weights
 
 
+def _new(shape, dtype, device):
+    """torch.empty of two dimensions (the strided form costs about half as much)."""
+    import torch
+
+    return torch.empty_strided(shape, (shape[1], 1), dtype=dtype, device=device)
+
+
 def quantize_fp8(x, square: bool = False, transpose: bool = False, rmsnorm: bool = False, rms_gain=None,
                  rms_eps: float = 1e-6, stream=None):
     """(q, s) of x [R, C] (float32 or bfloat16), or (q, s, qt, st) with `transpose`."""
@@ -593,12 +601,14 @@ def quantize_fp8(x, square: bool = False, transpose: bool = False, rmsnorm: bool
 
     R, C = x.shape
     rb, cb, ldq, ldt = (R + 127) // 128, (C + 127) // 128, (C + 15) // 16 * 16, (R + 15) // 16 * 16
-    dev, f8, f32, bf16 = x.device, torch.float8_e4m3fn, torch.float32, x.dtype is torch.bfloat16
+    dev, f8, f32, bf16 = x.get_device(), torch.float8_e4m3fn, torch.float32, x.dtype is torch.bfloat16
     flags = ((FLAG_FP8_SQUARE if square else 0) | (FLAG_RMSNORM if rmsnorm else 0) | (FLAG_BF16_INPUT if bf16 else 0))
-    q, s = x.new_empty((R, ldq), dtype=f8), x.new_empty((rb, cb) if square else (cb, R), dtype=f32)
+    q = _new((R, ldq), f8, x.device)
+    s = _new((rb, cb) if square else (cb, R), f32, x.device)
     qt = st = None
     if transpose:
-        qt, st = x.new_empty((C, ldt), dtype=f8), x.new_empty((cb, rb) if square else (rb, C), dtype=f32)
+        qt = _new((C, ldt), f8, x.device)
+        st = _new((cb, rb) if square else (rb, C), f32, x.device)
     _call("tq_quantize_fp8", dev, stream, _fit(x, torch.bfloat16 if bf16 else f32, (R, C), dev, "x"), R, C, flags,
           None if rms_gain is None else _fit(rms_gain, f32, (C,), dev, "rms_gain"), rms_eps, q.data_ptr(), s.data_ptr(),
           qt.data_ptr() if transpose else None, st.data_ptr() if transpose else None)
@@ -609,6 +619,6 @@ def fp8_gemm(xq, s_x, wq, s_w, K: int, w_rows: bool = False, bf16: bool = False,
     """y [M, N] of codes and scales as quantize_fp8 gives them (w: its square form, or with `w_rows` its row form)."""
     import torch
 
-    y = xq.new_empty((xq.shape[0], wq.shape[0]), dtype=torch.bfloat16 if bf16 else torch.float32)
+    y = _new((xq.shape[0], wq.shape[0]), torch.bfloat16 if bf16 else torch.float32, xq.device)
     fp8_gemm_(xq, s_x, wq, s_w, K, (FLAG_FP8_W_ROWS if w_rows else 0) | (FLAG_BF16_OUTPUT if bf16 else 0), y, stream)
     return y
