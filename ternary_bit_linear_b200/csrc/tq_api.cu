@@ -1430,6 +1430,8 @@ tq_status tq_moe_swiglu(const float *x, int64_t M, int64_t d_model, int64_t d_ff
     a.F = (int)d_ffn;
     a.E = (int)n_experts;
     a.k = (int)top_k;
+    a.inv_d = 1.0 / (double)d_model;
+    a.inv_f = 1.0 / (double)d_ffn;
     a.per_row = pr ? 1 : 0;
     a.norm_topk = (flags & TQ_FLAG_NORM_TOPK) ? 1 : 0;
     a.enc = enc;

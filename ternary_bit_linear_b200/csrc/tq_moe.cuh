@@ -71,6 +71,7 @@ struct MoeArgs {
     float *weights;
     int M, D, F, E, k;
     int per_row, norm_topk, enc;
+    double inv_d, inv_f;  // 1 / D, 1 / F
     float clamp_val;
     ActParams act;
     // workspace
@@ -96,11 +97,17 @@ struct MoeRed {
     double d[kMoeWarps];
 };
 
+// Warp-wide maximum of non-negative values: their bits order as unsigned numbers
+// (a NaN's above all), and one instruction replaces five exchanges.
+__device__ __forceinline__ float warp_max_nonneg(float v) {
+    return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+}
+
 // FWHT-512 and int8 codes of a row held by a team of nw warps (warp wt has block
 // wt, 16 values per lane as in tq_act.cuh; red: the team's slots).  The steps and
 // roundings of tq_prologue_fwht_kernel; the codes are written in the small-M
 // GEMV's layout.
-__device__ __forceinline__ void moe_rot_quant(float (&f)[16], int wt, int nw, int bar, const ActParams &p, int K,
+__device__ __forceinline__ void moe_rot_quant(float (&f)[16], int wt, int nw, int bar, const ActParams &p, double inv_k,
                                               int8_t *__restrict__ dst, float *__restrict__ s, int32_t *__restrict__ rowsum,
                                               float *redf, int *redi, double *redd) {
     const int lane = threadIdx.x & 31;
@@ -120,7 +127,7 @@ __device__ __forceinline__ void moe_rot_quant(float (&f)[16], int wt, int nw, in
         for (int off = 8; off > 0; off >>= 1) ss = __dadd_rn(ss, __shfl_xor_sync(0xffffffffu, ss, off));
         ss = __shfl_sync(0xffffffffu, ss, 0);
         // within 2 units of fp64 of 1 / sqrt(ss / K + eps)
-        const double r = rsqrt(__fma_rn(ss, 1.0 / (double)K, (double)p.rms_eps));
+        const double r = rsqrt(__fma_rn(ss, inv_k, (double)p.rms_eps));
 #pragma unroll
         for (int i = 0; i < 16; ++i) f[i] = __double2float_rn(__dmul_rn((double)f[i], r));
     }
@@ -128,10 +135,10 @@ __device__ __forceinline__ void moe_rot_quant(float (&f)[16], int wt, int nw, in
     float amax = 0.0f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
-    amax = warp_max(amax);
+    amax = warp_max_nonneg(amax);
     if (lane == 0) redf[wt] = amax;
     bar_sync_n(bar, 32 * nw);
-    amax = warp_max(lane < nw ? redf[lane] : 0.0f);
+    amax = warp_max_nonneg(lane < nw ? redf[lane] : 0.0f);
     const float eta = eta_of(amax, p);
     const float scale = __fdiv_rn(127.0f, eta);
     uint32_t *out = reinterpret_cast<uint32_t *>(dst);
@@ -152,11 +159,11 @@ __device__ __forceinline__ void moe_rot_quant(float (&f)[16], int wt, int nw, in
         const int idx = wt * 128 + j * 32 + lane, e = lane & 3;
         out[4 * gemv_chunk_pos(idx >> 2) + e] = e == 0 ? t.x : e == 1 ? t.y : e == 2 ? t.z : t.w;
     }
-    sum = warp_sum_i(sum);
+    sum = __reduce_add_sync(0xffffffffu, sum);
     if (lane == 0) redi[wt] = sum;
     bar_sync_n(bar, 32 * nw);
     if (wt == 0) {
-        sum = warp_sum_i(lane < nw ? redi[lane] : 0);
+        sum = __reduce_add_sync(0xffffffffu, lane < nw ? redi[lane] : 0);
         if (lane == 0) {
             *s = __fdiv_rn(eta, 127.0f);
             *rowsum = sum;
@@ -193,7 +200,7 @@ __global__ void __launch_bounds__(kMoeThreads) tq_moe_route_kernel(const __grid_
         if (warp >= nw) return;
         float f[16];
         load_block16(f, a.x + (int64_t)m * a.D, warp);
-        moe_rot_quant(f, warp, nw, 1, a.act, a.D, a.xq + (int64_t)m * a.D, a.sx + m, a.rs + m, red.f, red.i, red.d);
+        moe_rot_quant(f, warp, nw, 1, a.act, a.inv_d, a.xq + (int64_t)m * a.D, a.sx + m, a.rs + m, red.f, red.i, red.d);
         return;
     }
     const int u = blockIdx.x - a.M, tgroups = (a.M + kMoeRouteTokens - 1) / kMoeRouteTokens;
@@ -714,7 +721,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) tq_moe_experts_kernel(const __
                 if (sm.ids[p] < 0) continue;
                 float f[16];
                 load_block16(f, a.h + (int64_t)p * a.F, wt);
-                moe_rot_quant(f, wt, nw, 1 + team, a.act, a.F, a.hq + (int64_t)p * a.F, a.sh + p, a.rh + p,
+                moe_rot_quant(f, wt, nw, 1 + team, a.act, a.inv_f, a.hq + (int64_t)p * a.F, a.sh + p, a.rh + p,
                               sm.red.f + team * nw, sm.red.i + team * nw, sm.red.d + team * nw);
                 bar_sync_n(1 + team, 32 * nw);  // the slots of red are written again
             }
