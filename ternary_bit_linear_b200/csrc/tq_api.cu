@@ -1452,7 +1452,7 @@ tq_status tq_moe_swiglu(const float *x, int64_t M, int64_t d_model, int64_t d_ff
     a.rh = reinterpret_cast<int32_t *>(ws + off[8]);
     a.out = reinterpret_cast<float *>(ws + off[9]);
     cudaStream_t st = cs(stream);
-    const int64_t units = router ? (n_experts + kMoeWarps - 1) / kMoeWarps * ((M + kMoeRouteTokens - 1) / kMoeRouteTokens) : 0;
+    const int64_t units = router ? (n_experts + kMoeRouteExperts - 1) / kMoeRouteExperts * ((M + kMoeRouteTokens - 1) / kMoeRouteTokens) : 0;
     if (tq_status e = launch_pdl(tq_moe_route_kernel, dim3((unsigned)(M + units)), dim3(kMoeThreads), 0, st, a)) return e;
     if (d_model <= kMoeRingK && d_ffn <= kMoeRingK)
         return enc != kEncFoundry ? launch_moe_experts<true, 4>(a, sms, st) : launch_moe_experts<false, 4>(a, sms, st);

@@ -18,7 +18,7 @@
 // bytes each); for one or two tokens, the chain of dependent steps.
 //
 //   tq_moe_route_kernel: a CTA per token quantises it; the other CTAs compute the
-//     logits of 16 experts and four tokens each.
+//     logits of 8 experts and four tokens each.
 //   tq_moe_experts_kernel: one CTA per SM, launched cooperatively (all CTAs
 //     resident), with grid-wide barriers between its phases:
 //       choice     every CTA picks every token's experts (for up to 16 tokens that is
@@ -57,7 +57,7 @@ constexpr int kMoeMaxPairs = kMoeMaxTokens * kMoeMaxTopk;
 constexpr int kMoeChunk = 8;  // pairs of one expert per problem: the MMA's 8 columns
 constexpr int kMoeMaxProblems = kMoeMaxExperts + kMoeMaxPairs / kMoeChunk;
 constexpr int kMoeMaxK = 8192;  // d_model, d_ffn: 16 blocks of 512, one per warp
-constexpr int kMoeRouteTokens = 4;
+constexpr int kMoeRouteTokens = 4, kMoeRouteExperts = 8;  // logits per CTA
 constexpr int kMoeSlot = 8 * 32;  // 32-bit words of a warp's exchange slot
 constexpr int kMoeRedBytes = kMoeWarps * kMoeSlot * 4;
 static_assert(kMoeRedBytes >= kMoeMaxPairs / 32 * kMoeMaxExperts * 2, "the pair counts fit the exchange slots");
@@ -184,13 +184,13 @@ __device__ __forceinline__ void load_block16(float (&f)[16], const float *row, i
     }
 }
 
-// CTAs 0 .. M - 1: token blockIdx.x's codes.  The others: logits of 16 experts and
-// 4 tokens, a warp for 4 experts and a quarter of d_model (so that a converted
-// value enters four products, and few tokens still spread over many lanes); the
-// quarters are added in order.
-__global__ void __launch_bounds__(kMoeThreads) tq_moe_route_kernel(const __grid_constant__ MoeArgs a) {
+// CTAs 0 .. M - 1: token blockIdx.x's codes.  The others: logits of 8 experts and
+// 4 tokens, a warp for 2 experts and a quarter of d_model (so that few tokens
+// still spread over many lanes); the quarters are added in order.  Two CTAs per
+// SM: the largest batches of 128 experts then take little more than one wave.
+__global__ void __launch_bounds__(kMoeThreads, 2) tq_moe_route_kernel(const __grid_constant__ MoeArgs a) {
     __shared__ MoeRed red;
-    __shared__ double part[kMoeWarps][4 * kMoeRouteTokens];
+    __shared__ double part[kMoeWarps][2 * kMoeRouteTokens];
     pdl_wait();
     pdl_trigger();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -204,23 +204,23 @@ __global__ void __launch_bounds__(kMoeThreads) tq_moe_route_kernel(const __grid_
         return;
     }
     const int u = blockIdx.x - a.M, tgroups = (a.M + kMoeRouteTokens - 1) / kMoeRouteTokens;
-    const int e0 = u / tgroups * kMoeWarps + (warp >> 2) * 4, m0 = u % tgroups * kMoeRouteTokens;
+    const int e0 = u / tgroups * kMoeRouteExperts + (warp >> 2) * 2, m0 = u % tgroups * kMoeRouteTokens;
     const int nt = a.M - m0 < kMoeRouteTokens ? a.M - m0 : kMoeRouteTokens;
     const int nv = a.D / 4, q0 = (warp & 3) * (nv / 4);  // float4; a quarter is a multiple of 32
-    const float4 *wr[4];
+    const float4 *wr[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)  // experts past the last: the last again, not stored
+    for (int i = 0; i < 2; ++i)  // experts past the last: the last again, not stored
         wr[i] = reinterpret_cast<const float4 *>(a.router + (int64_t)(e0 + i < a.E ? e0 + i : a.E - 1) * a.D) + q0 + lane;
     const float4 *xr = reinterpret_cast<const float4 *>(a.x + (int64_t)m0 * a.D) + q0 + lane;
-    double s[4][kMoeRouteTokens];
+    double s[2][kMoeRouteTokens];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int t = 0; t < kMoeRouteTokens; ++t) s[i][t] = 0.0;
     for (int c = 0; c < nv / 4; c += 32) {
-        float4 w[4], v[kMoeRouteTokens];
+        float4 w[2], v[kMoeRouteTokens];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __ldg(wr[i] + c);
+        for (int i = 0; i < 2; ++i) w[i] = __ldg(wr[i] + c);
 #pragma unroll
         for (int t = 0; t < kMoeRouteTokens; ++t)
             if (t < nt) v[t] = __ldg(xr + (int64_t)t * nv + c);
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kMoeThreads) tq_moe_route_kernel(const __grid_
             if (t >= nt) break;
             if (a.act.sanitize) v[t] = quench4(v[t], a.act);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
                 s[i][t] = __fma_rn((double)v[t].x, (double)w[i].x, s[i][t]);
                 s[i][t] = __fma_rn((double)v[t].y, (double)w[i].y, s[i][t]);
                 s[i][t] = __fma_rn((double)v[t].z, (double)w[i].z, s[i][t]);
@@ -241,17 +241,17 @@ __global__ void __launch_bounds__(kMoeThreads) tq_moe_route_kernel(const __grid_
     for (int t = 0; t < kMoeRouteTokens; ++t) {
         if (t >= nt) break;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < 2; ++i) {
             const double v = warp_sum_d(s[i][t]);
-            if (lane == 0) part[warp][4 * t + i] = v;
+            if (lane == 0) part[warp][2 * t + i] = v;
         }
     }
     __syncthreads();
-    if (threadIdx.x < 16 * nt) {
-        const int t = threadIdx.x >> 4, i = threadIdx.x & 15, e = u / tgroups * kMoeWarps + i;
+    if (threadIdx.x < kMoeRouteExperts * nt) {
+        const int t = threadIdx.x / kMoeRouteExperts, i = threadIdx.x % kMoeRouteExperts, e = u / tgroups * kMoeRouteExperts + i;
         double v = 0.0;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v = __dadd_rn(v, part[(i >> 2) * 4 + q][4 * t + (i & 3)]);
+        for (int q = 0; q < 4; ++q) v = __dadd_rn(v, part[(i >> 1) * 4 + q][2 * t + (i & 1)]);
         if (e < a.E) a.logits[(int64_t)(m0 + t) * a.E + e] = __double2float_rn(v);
     }
 }
