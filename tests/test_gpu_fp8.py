@@ -251,3 +251,44 @@ def test_training_step(cuda_lib, M, N, K, bf16):
         # two quantised factors, 2^-4 of each element's value (or, for the smallest, of the block's smallest step)
         bound = (mag * u.abs()).sum() * (2 * 2.0 ** -4 + 2.0 ** -8)
         assert abs((grad.double() * u).sum() - step / (2 * h)) <= bound
+
+
+@pytest.mark.parametrize("R,C", [(1, 300001), (300001, 1), (2, 131072)])
+def test_quantize_long(cuda_lib, R, C):
+    tq = cuda_lib
+    x = normal(R + C, R, C)
+    check_quant(*tq.quantize_fp8(x), x, False)
+    q, s, qt, st = tq.quantize_fp8(x, square=True, transpose=True)
+    check_quant(q, s, x, True)
+    check_quant(qt, st, x.t().contiguous(), True)
+
+
+@pytest.mark.parametrize("M,N,K", [(2, 40, 300000), (90, 70, 100001)])
+def test_product_long(cuda_lib, M, N, K):
+    tq = cuda_lib
+    for w_rows in (False, True):
+        xq, sx, wq, sw, xv, wv = operands(tq, M, N, K, w_rows)
+        check_product(tq.fp8_gemm(xq, sx, wq, sw, K, w_rows=w_rows), xv, wv, K)
+    assert tq.device_status() == 0
+
+
+def test_past_32_bit_offsets(cuda_lib):
+    """More than 2^31 elements in, and out: the last rows against the same rows alone."""
+    tq = cuda_lib
+    R, C = 132000, 16400
+    x = torch.empty(R, C, dtype=torch.bfloat16, device="cuda")
+    x[:1000] = 0
+    x[-300:] = normal(1, 300, C).bfloat16()
+    q, s = tq.quantize_fp8(x)
+    q2, s2 = tq.quantize_fp8(x[-300:].contiguous())
+    assert torch.equal(q[-300:].view(torch.uint8), q2.view(torch.uint8)) and torch.equal(s[:, -300:], s2)
+    del x, q, s
+    M, N, K = 66000, 33000, 16
+    a, b = normal(2, M, K), normal(3, N, K)
+    aq, sa = tq.quantize_fp8(a)
+    bq, sb = tq.quantize_fp8(b, square=True)
+    y = tq.fp8_gemm(aq, sa, bq, sb, K, bf16=True)
+    av, bv = values(aq[:, :K], sa.t(), 1, 128), values(bq[:, :K], sb, 128, 128)
+    check_product(y[-300:], av[-300:], bv, K)
+    check_product(y[:300, -300:], av[:300], bv[-300:], K)
+    assert tq.device_status() == 0

@@ -106,12 +106,16 @@ CASES = [  # M, D, F, E, k, per_row, rms, norm
     (3, 1024, 512, 5, 5, True, False, False),
     (7, 2048, 1024, 64, 8, True, True, True),
     (64, 512, 512, 256, 8, False, True, True),
-    (33, 1536, 2048, 4, 2, True, True, False),      # problems of 16 pairs and a rest
+    (33, 1536, 2048, 4, 2, True, True, False),      # several problems per expert and a rest
     (17, 512, 8192, 3, 1, False, True, True),       # the longest rows of the down projection
     (5, 8192, 512, 4, 2, True, True, True),         # and of the others
     (64, 512, 512, 2, 2, True, True, True),         # every token on every expert
     (64, 1024, 1536, 40, 16, False, False, True),   # the most slots
     (2, 4608, 2560, 9, 3, True, True, False),       # teams of 9 and 5 warps
+    (64, 512, 1024, 3, 2, False, True, True),       # many pairs per expert: several problems of each
+    (33, 4608, 1536, 2, 1, True, True, True),       # ... with the short ring of long rows
+    (64, 1024, 7168, 5, 1, True, False, False),
+    (40, 8192, 1024, 2, 2, False, True, True),
 ]
 
 
@@ -281,3 +285,42 @@ def test_agrees_with_the_dense_block(cuda_lib):
     _, s = quant(act, True)
     flips = F // 128  # codes that could move, generously: 127 * 4 ulp of a value near a border, over F of them
     assert ((y - dense).abs() <= flips * layers[2][1] * s * 1.001 + dense.abs() * 1e-5).all()
+
+
+def test_every_pair_on_one_expert(cuda_lib):
+    """The most pairs one expert can get: 64 tokens with all 16 slots on it."""
+    tq = cuda_lib
+    M, D, F, E, k = 64, 512, 512, 20, 16
+    x, _, layers = make(21, M, D, F, E, True)
+    ids = torch.full((M, k), 13, dtype=torch.int32, device="cuda")
+    w = torch.rand(M, k, generator=gen(2), device="cuda")
+    fl = tq.FLAG_FWHT | tq.FLAG_RMSNORM | tq.GAMMA_PER_ROW
+    y = torch.empty_like(x)
+    ws = torch.empty(tq.moe_workspace_bytes(M, D, F, E, k, fl), dtype=torch.uint8, device="cuda")
+    tq.moe_swiglu_(x, None, *layers, fl, y, ids, w, ws)
+    ref, mag, _, _ = reference(x, None, layers, k, True, True, True, 0, ids=ids.long(), w=w)
+    check_y(y, ref, mag, k)
+    assert tq.device_status() == 0
+
+
+def test_weights_past_32_bit_offsets(cuda_lib):
+    """160 experts of 8192 x 8192: 2.7 GB per stacked matrix.  Two experts are filled in, the first and the last."""
+    tq = cuda_lib
+    M, D, F, E, k = 3, 8192, 8192, 160, 2
+    x, _, small = make(31, M, D, F, 2, True)
+    layers = []
+    for p, s in small:
+        big = torch.empty((E,) + tuple(p.shape[1:]), dtype=torch.uint8, device="cuda")
+        sb = torch.empty((E, s.shape[1]), device="cuda")
+        big[0], big[E - 1], sb[0], sb[E - 1] = p[0], p[1], s[0], s[1]
+        layers.append((big, sb))
+    ids = torch.tensor([[0, E - 1], [E - 1, 0], [E - 1, E]], dtype=torch.int32, device="cuda")
+    w = torch.rand(M, k, generator=gen(3), device="cuda")
+    fl = tq.FLAG_FWHT | tq.FLAG_RMSNORM | tq.GAMMA_PER_ROW
+    y = torch.empty_like(x)
+    ws = torch.empty(tq.moe_workspace_bytes(M, D, F, E, k, fl), dtype=torch.uint8, device="cuda")
+    tq.moe_swiglu_(x, None, *layers, fl, y, ids, w, ws)
+    near = torch.where(ids == E - 1, 1, torch.where(ids == 0, 0, -1)).long()
+    ref, mag, _, _ = reference(x, None, small, k, True, True, True, 0, ids=near, w=w)
+    check_y(y, ref, mag, k)
+    assert tq.device_status() == 0
