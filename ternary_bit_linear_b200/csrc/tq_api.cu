@@ -605,11 +605,11 @@ inline bool moe_shape_ok(int64_t M, int64_t D, int64_t F, int64_t E, int64_t k) 
 
 constexpr int kMoeRingK = 4096;  // longest token rows that leave room for a ring of four steps
 
-template <bool CONV, int PD>
-tq_status launch_moe_experts(const MoeArgs &a, int sms, cudaStream_t st) {
+template <bool CONV, int PD, bool FEW>
+tq_status launch_moe_experts_as(const MoeArgs &a, int sms, cudaStream_t st) {
     static std::atomic<int> attr_done[kMaxDevices];
     constexpr int kFixed = kMoeRedBytes + kMoeWarps * PD * 2048, kMostK = PD == 4 ? kMoeRingK : kMoeMaxK;
-    if (tq_status e = set_smem_once(tq_moe_experts_kernel<CONV, PD>, kFixed + 2 * kMoeChunk * (kMostK + 128), attr_done)) return e;
+    if (tq_status e = set_smem_once(tq_moe_experts_kernel<CONV, PD, FEW>, kFixed + 2 * kMoeChunk * (kMostK + 128), attr_done)) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)sms);
     cfg.blockDim = dim3(kMoeThreads);
@@ -620,7 +620,12 @@ tq_status launch_moe_experts(const MoeArgs &a, int sms, cudaStream_t st) {
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tq_moe_experts_kernel<CONV, PD>, a) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+    return cudaLaunchKernelEx(&cfg, tq_moe_experts_kernel<CONV, PD, FEW>, a) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}
+
+template <bool CONV, int PD>
+tq_status launch_moe_experts(const MoeArgs &a, int sms, cudaStream_t st) {
+    return a.M * a.k <= kMoeFew ? launch_moe_experts_as<CONV, PD, true>(a, sms, st) : launch_moe_experts_as<CONV, PD, false>(a, sms, st);
 }
 
 // ---------------------------------------------------------------------------

@@ -32,6 +32,9 @@
 //       down       strips of 32 rows, runs as before.
 //       sum        y from the pairs' outputs, slots in order: no atomics, and
 //                  the result does not depend on how pairs were grouped.
+//       For up to 16 pairs, where it costs few steps more, a CTA contracts a strip
+//       of down for every pair at once and adds them itself: down and sum without
+//       the barrier between them (one token of 512 x 1024: 16.9 us, 18.9 us apart).
 //   A warp streams its strips' weights from HBM by asynchronous copies into a ring
 //   of its own, two or four column steps (of 2 KB) ahead, across strips and problems,
 //   and into the down phase from before the rotation; a lane reads only what it
@@ -55,6 +58,7 @@ constexpr int kMoeThreads = 32 * kMoeWarps;
 constexpr int kMoeMaxTokens = 64, kMoeMaxTopk = 16, kMoeMaxExperts = 256;
 constexpr int kMoeMaxPairs = kMoeMaxTokens * kMoeMaxTopk;
 constexpr int kMoeChunk = 8;  // pairs of one expert per problem: the MMA's 8 columns
+constexpr int kMoeFew = 2 * kMoeChunk;  // pairs whose codes fit the two buffers at once: tq_moe_experts_kernel<.., FEW>
 constexpr int kMoeMaxProblems = kMoeMaxExperts + kMoeMaxPairs / kMoeChunk;
 constexpr int kMoeMaxK = 8192;  // d_model, d_ffn: 16 blocks of 512, one per warp
 constexpr int kMoeRouteTokens = 4, kMoeRouteExperts = 8;  // logits per CTA
@@ -347,6 +351,7 @@ struct MoeShared {
     int16_t sorted[kMoeMaxPairs];
     int16_t count[kMoeMaxExperts], first[kMoeMaxExperts];
     MoeProblem prob[kMoeMaxProblems];
+    int16_t where[kMoeFew];  // of up to so many pairs: problem << 8 | place in it
     int nprob, flag;
     MoeRed red;
 };
@@ -386,9 +391,33 @@ __device__ __forceinline__ MoeRun moe_run(const MoeArgs &a, const MoeShared &sm)
     return r;
 }
 
+// The down phase with its sum: this CTA's strips blockIdx.x, + gridDim.x, ..., a team
+// of warps per problem.  False where a warp's steps are more
+// than four above the other form's: 8 tokens of 1536 x 6144, 12 steps to 6, took
+// 39.6 us to 37.4 us; 4 of 2048 x 1536, 3 steps to 3, 24.0 us to 26.5 us.
+// `r` is the other form's run, and becomes this one's.
+__device__ __forceinline__ bool moe_run_joint(const MoeArgs &a, const MoeShared &sm, MoeRun &r) {
+    if (sm.nprob == 0) return false;
+    const int steps = a.F / 256, n = (int)gridDim.x, warp = threadIdx.x >> 5;
+    int ks = kMoeWarps;
+    while (ks > 1 && (kMoeWarps / ks < sm.nprob || ks > steps)) ks >>= 1;
+    const int T = kMoeWarps / r.ks, run = (sm.nprob * r.spp + n - 1) / n;
+    if ((r.spp + n - 1) / n * ((steps + ks - 1) / ks) > (run + T - 1) / T * ((steps + r.ks - 1) / r.ks) + 4) return false;
+    r.ks = ks;
+    r.team = warp / r.ks;
+    r.kw = warp % r.ks;
+    r.mine = (steps - r.kw + r.ks - 1) / r.ks;
+    r.q = r.team;
+    r.s1 = (r.q + 1) * r.spp;
+    r.strip = (int)blockIdx.x;
+    r.end = r.team < sm.nprob ? r.spp : 0;
+    r.i = 0;
+    return true;
+}
+
 // Requests the next step of this warp's run into a slot of its ring: one group, an
 // empty one past the end.
-template <bool GATE>
+template <bool GATE, bool JOINT = false>
 __device__ __forceinline__ void moe_load(const MoeArgs &a, const MoeShared &sm, MoeRun &r, uint32_t slot) {
     while (r.strip >= r.end) {  // on to the next problem of the run
         if ((r.q + 1) * r.spp >= r.s1) break;
@@ -407,7 +436,7 @@ __device__ __forceinline__ void moe_load(const MoeArgs &a, const MoeShared &sm, 
         cp_async16(slot + 1536, q + 8 * KB);
         if (++r.i == r.mine) {
             r.i = 0;
-            r.strip += kMoeWarps / r.ks;
+            r.strip += JOINT ? (int)gridDim.x : kMoeWarps / r.ks;
         }
     }
     cp_async_commit();
@@ -422,6 +451,62 @@ __device__ __forceinline__ void moe_stage(const MoeArgs &a, const MoeShared &sm,
         const int p = sm.sorted[pb.start + r];
         cp_async16(x_s + (uint32_t)(r * XS + 16 * c), (GATE ? a.xq + (int64_t)(p / a.k) * K : a.hq + (int64_t)p * K) + 16 * c);
     }
+}
+
+// This warp's sums of a strip: its steps from the ring, which goes on behind them.
+template <bool GATE, bool JOINT, bool CONV, int PD>
+__device__ __forceinline__ void moe_strip_sums(const MoeArgs &a, const MoeShared &sm, MoeRun &run, uint32_t ring, int &slot,
+                                               uint32_t xr, uint32_t xsw, int (&acc)[2][4]) {
+    int d[4][2][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[j][0][i] = d[j][1][i] = 0;
+#pragma unroll 1
+    for (int i = 0; i < run.mine; ++i) {
+        cp_async_wait_groups<PD - 1>();
+        const uint32_t from = ring + (uint32_t)(slot * 2048);
+        moe_step_mma<CONV>(d, from, xr + (uint32_t)(256 * run.ks * i), xsw, a.enc);
+        moe_load<GATE, JOINT>(a, sm, run, from);  // the slot takes the step PD ahead
+        slot = slot + 1 == PD ? 0 : slot + 1;
+    }
+#pragma unroll
+    for (int mat = 0; mat < 2; ++mat)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)  // exact: d[j] is a multiple of 4^j
+            acc[mat][i] = d[0][mat][i] + (d[1][mat][i] >> 2) + (d[2][mat][i] >> 4) + (d[3][mat][i] >> 6);
+}
+
+// The team's sums, in its first warp.
+__device__ __forceinline__ void moe_team_sums(int (&acc)[2][4], const MoeRun &run, int *red) {
+    if (run.ks == 1) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (run.kw != 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) red[warp * kMoeSlot + i * 32 + lane] = acc[i >> 2][i & 3];
+    }
+    bar_sync_n(1 + run.team, 32 * run.ks);
+    if (run.kw == 0) {
+        for (int w2 = warp + 1; w2 < warp + run.ks; ++w2)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] += red[w2 * kMoeSlot + i * 32 + lane];
+    }
+    bar_sync_n(1 + run.team, 32 * run.ks);  // the slots are written again
+}
+
+// A strip's projections (matrix, row, token) at [matrix][token / 2][(16 (token % 2) + row + 8 (token / 2)) % 32].
+__device__ __forceinline__ int moe_value_at(int tok, int row) { return 32 * (tok >> 1) + ((16 * (tok & 1) + row + 8 * (tok >> 1)) & 31); }
+__device__ __forceinline__ void moe_values(float *val, const int (&acc)[2][4], const float (&ga)[2], const float (&gb)[2],
+                                           const float (&sv)[2], const int (&rv)[2]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int hi = 0; hi < 2; ++hi)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int c = 2 * hi + e, to = moe_value_at(2 * t + e, g + 8 * hi);
+            val[to] = __fmul_rn(__int2float_rn(acc[0][c] - rv[e]), __fmul_rn(ga[hi], sv[e]));
+            val[128 + to] = __fmul_rn(__int2float_rn(acc[1][c] - rv[e]), __fmul_rn(gb[hi], sv[e]));
+        }
 }
 
 // The run, the first PD steps of each warp requested before.  While a problem's
@@ -472,63 +557,24 @@ __device__ __forceinline__ void moe_contract(const MoeArgs &a, const MoeShared &
                 ga[hi] = __ldg((GATE ? a.gate_gamma : a.down_gamma) + n);
                 gb[hi] = __ldg(GATE ? a.up_gamma + n : a.down_gamma + n + (a.per_row ? 16 : 0));
             }
-            int d[4][2][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) d[j][0][i] = d[j][1][i] = 0;
-#pragma unroll 1
-            for (int i = 0; i < run.mine; ++i) {
-                cp_async_wait_groups<PD - 1>();
-                const uint32_t from = ring + (uint32_t)(slot * 2048);
-                moe_step_mma<CONV>(d, from, xr + (uint32_t)(256 * ks * i), xsw, a.enc);
-                moe_load<GATE>(a, sm, run, from);  // the slot takes the step PD ahead
-                slot = slot + 1 == PD ? 0 : slot + 1;
-            }
-            committed += run.mine;
             int acc[2][4];
-#pragma unroll
-            for (int mat = 0; mat < 2; ++mat)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)  // exact: d[j] is a multiple of 4^j
-                    acc[mat][i] = d[0][mat][i] + (d[1][mat][i] >> 2) + (d[2][mat][i] >> 4) + (d[3][mat][i] >> 6);
-            if (ks > 1) {
-                if (kw != 0) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) red[warp * kMoeSlot + i * 32 + lane] = acc[i >> 2][i & 3];
-                }
-                bar_sync_n(1 + team, 32 * ks);
-                if (kw == 0) {
-                    for (int w2 = warp + 1; w2 < warp + ks; ++w2)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) acc[i >> 2][i & 3] += red[w2 * kMoeSlot + i * 32 + lane];
-                }
-                bar_sync_n(1 + team, 32 * ks);  // the slots are written again
-            }
+            moe_strip_sums<GATE, false, CONV, PD>(a, sm, run, ring, slot, xr, xsw, acc);
+            committed += run.mine;
+            moe_team_sums(acc, run, red);
             if (kw != 0) continue;
             // The projections' values pass through this warp's own slot, so that the
-            // lanes share what follows evenly and stores cover whole rows' stretches:
-            // value (mat, row, token) at [mat][token / 2][(16 (token % 2) + row + 8 (token / 2)) % 32].
+            // lanes share what follows evenly and stores cover whole rows' stretches.
             __syncwarp();  // the slot's last readers are done
-#pragma unroll
-            for (int hi = 0; hi < 2; ++hi)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int c = 2 * hi + e, to = 32 * t + ((16 * e + g + 8 * hi + 8 * t) & 31);
-                    val[to] = __fmul_rn(__int2float_rn(acc[0][c] - rv[e]), __fmul_rn(ga[hi], sv[e]));
-                    val[128 + to] = __fmul_rn(__int2float_rn(acc[1][c] - rv[e]), __fmul_rn(gb[hi], sv[e]));
-                }
+            moe_values(val, acc, ga, gb, sv, rv);
             __syncwarp();
             if (GATE) {
                 for (int i = lane; i < 16 * pb.count; i += 32) {
-                    const int tok = i >> 4, row = i & 15, h = tok >> 1;
-                    const int from = 32 * h + ((16 * (tok & 1) + row + 8 * h) & 31);
+                    const int tok = i >> 4, row = i & 15, from = moe_value_at(tok, row);
                     a.h[(int64_t)sm.sorted[pb.start + tok] * N + n0 + row] = moe_act(val[from], val[128 + from], a.clamp_val);
                 }
             } else {
                 for (int tok = 0; tok < pb.count; ++tok) {
-                    const int h = tok >> 1, from = 32 * h + ((16 * (tok & 1) + (lane & 15) + 8 * h) & 31);
-                    a.out[(int64_t)sm.sorted[pb.start + tok] * N + n0 + lane] = val[128 * (lane >> 4) + from];
+                    a.out[(int64_t)sm.sorted[pb.start + tok] * N + n0 + lane] = val[128 * (lane >> 4) + moe_value_at(tok, lane & 15)];
                 }
             }
         }
@@ -545,8 +591,69 @@ __device__ __forceinline__ void moe_contract(const MoeArgs &a, const MoeShared &
     }
 }
 
-// PD: column steps in each warp's ring (4, or 2 where longer token rows need the room).
+// The down phase with its sum (moe_run_joint), the first steps requested before.
 template <bool CONV, int PD>
+__device__ __forceinline__ void moe_down_joint(const MoeArgs &a, const MoeShared &sm, MoeRun &run, uint32_t ring, uint32_t x_s,
+                                               int *red) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int K = a.F, XS = gemv_x_stride(K), cpr = K >> 4;
+    const MoeProblem last = sm.prob[sm.nprob - 1];
+    // every pair's codes, at most 16 rows (the two buffers' room), in sorted order
+    for (int i = threadIdx.x; i < (last.start + last.count) * cpr; i += kMoeThreads) {
+        const int r = i / cpr, c = i - r * cpr;
+        cp_async16(x_s + (uint32_t)(r * XS + 16 * c), a.hq + (int64_t)sm.sorted[r] * K + 16 * c);
+    }
+    cp_async_commit();
+    const bool active = run.team < sm.nprob;
+    const MoeProblem pb = sm.prob[active ? run.team : 0];
+    float sv[2];
+    int rv[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int p = sm.sorted[pb.start + min(2 * t + e, pb.count - 1)];
+        sv[e] = __ldcg(a.sh + p);
+        rv[e] = __ldcg(a.rh + p);
+    }
+    const uint32_t xr = x_s + (uint32_t)((pb.start + min(g, pb.count - 1)) * XS + 64 * t + 256 * run.kw);
+    const uint32_t xsw = (uint32_t)(t & 2) << 4;
+    cp_async_wait_groups<0>();
+    __syncthreads();
+    int slot = 0;
+    for (int s = (int)blockIdx.x; s < run.spp; s += (int)gridDim.x) {
+        const int n0 = 32 * s;
+        if (active) {
+            float ga[2], gb[2];
+#pragma unroll
+            for (int hi = 0; hi < 2; ++hi) {
+                const int64_t n = a.per_row ? (int64_t)pb.expert * a.D + n0 + g + 8 * hi : pb.expert;
+                ga[hi] = __ldg(a.down_gamma + n);
+                gb[hi] = __ldg(a.down_gamma + n + (a.per_row ? 16 : 0));
+            }
+            int acc[2][4];
+            moe_strip_sums<false, true, CONV, PD>(a, sm, run, ring, slot, xr, xsw, acc);
+            moe_team_sums(acc, run, red);
+            if (run.kw == 0) moe_values(reinterpret_cast<float *>(red + warp * kMoeSlot), acc, ga, gb, sv, rv);
+        }
+        __syncthreads();
+        if (warp < a.M) {  // a warp per token, a lane per output
+            float y = 0.0f;
+            for (int j = 0; j < a.k; ++j) {
+                const int p = warp * a.k + j;
+                if (sm.ids[p] < 0) continue;
+                const int q = sm.where[p] >> 8, tok = sm.where[p] & 255;
+                const float *val = reinterpret_cast<const float *>(red + q * run.ks * kMoeSlot);
+                y = __fmaf_rn(sm.w[p], val[128 * (lane >> 4) + moe_value_at(tok, lane & 15)], y);
+            }
+            a.y[(int64_t)warp * a.D + n0 + lane] = y;
+        }
+        __syncthreads();  // the values are written again
+    }
+    cp_async_wait_groups<0>();
+}
+
+// PD: column steps in each warp's ring (4, or 2 where longer token rows need the room).
+// FEW: at most kMoeFew pairs.
+template <bool CONV, int PD, bool FEW>
 __global__ void __launch_bounds__(kMoeThreads, 1) tq_moe_experts_kernel(const __grid_constant__ MoeArgs a) {
     extern __shared__ __align__(128) uint8_t dyn[];
     __shared__ MoeShared sm;
@@ -631,71 +738,103 @@ __global__ void __launch_bounds__(kMoeThreads, 1) tq_moe_experts_kernel(const __
             sm.ids[p] = id >= 0 && id < a.E ? id : -1;
             sm.w[p] = __ldcg(a.weights + p);
         }
-    // Pairs by expert, in order (every CTA must come to the same grouping).  Warps
-    // rank the pairs of 32 at a time among those of the same expert and count them;
-    // a thread per expert turns its counts into offsets.
-    const int nch = (P + 31) / 32;
-    uint16_t *counts = reinterpret_cast<uint16_t *>(dyn);  // [nch][E]
-    for (int i = threadIdx.x; i < nch * a.E; i += kMoeThreads) counts[i] = 0;
-    __syncthreads();
-    int id_of[2] = {-1, -1}, rank[2] = {0, 0};  // chunks warp and warp + 16
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const int ch = warp + kMoeWarps * c, p = 32 * ch + lane;
-        if (ch >= nch) break;
-        const int id = p < P ? sm.ids[p] : -1;
-        const uint32_t same = __match_any_sync(0xffffffffu, id);
-        id_of[c] = id;
-        rank[c] = __popc(same & ((1u << lane) - 1u));
-        if (id >= 0 && rank[c] == 0) counts[ch * a.E + id] = (uint16_t)__popc(same);
-    }
-    __syncthreads();
-    if ((int)threadIdx.x < a.E) {
-        int n = 0;
-        for (int ch = 0; ch < nch; ++ch) {
-            const int c = counts[ch * a.E + threadIdx.x];
-            counts[ch * a.E + threadIdx.x] = (uint16_t)n;
-            n += c;
-        }
-        sm.count[threadIdx.x] = (int16_t)n;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        int at = 0, np = 0;  // running sums over experts
-        for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const int e = e0 + lane;
-            const int c = e < a.E ? sm.count[e] : 0, n = (c + kMoeChunk - 1) / kMoeChunk;
-            int cs = c, ns = n;
+    if constexpr (FEW) {
+        // One warp groups the pairs, experts in the order of their first pairs.
+        __syncthreads();
+        if (warp == 0) {
+            const int id = lane < P ? sm.ids[lane] : -1;
+            const uint32_t same = __match_any_sync(0xffffffffu, id);
+            const int rank = __popc(same & ((1u << lane) - 1u)), c = id >= 0 && rank == 0 ? __popc(same) : 0;
+            const int n = (c + kMoeChunk - 1) / kMoeChunk;
+            int both = c | (n << 16);  // running sums of pairs and of problems
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, cs, off), u = __shfl_up_sync(0xffffffffu, ns, off);
-                if (lane >= off) {
-                    cs += v;
-                    ns += u;
-                }
+                const int v = __shfl_up_sync(0xffffffffu, both, off);
+                if (lane >= off) both += v;
             }
-            if (e < a.E) {
-                sm.first[e] = (int16_t)(at + cs - c);
-                for (int i = 0; i < n; ++i) {
-                    MoeProblem pb;
-                    pb.expert = (int16_t)e;
-                    pb.start = (int16_t)(at + cs - c + i * kMoeChunk);
-                    pb.count = (int16_t)(c - i * kMoeChunk < kMoeChunk ? c - i * kMoeChunk : kMoeChunk);
-                    sm.prob[np + ns - n + i] = pb;
-                }
+            const int total = __shfl_sync(0xffffffffu, both, 31);
+            const int mine = both - (c | (n << 16)), lead = __shfl_sync(0xffffffffu, mine, __ffs(same) - 1);
+            if (id >= 0) {  // lanes below P
+                sm.sorted[(lead & 0xffff) + rank] = (int16_t)lane;
+                sm.where[lane] = (int16_t)(((lead >> 16) + rank / kMoeChunk) << 8 | rank % kMoeChunk);
             }
-            at += __shfl_sync(0xffffffffu, cs, 31);
-            np += __shfl_sync(0xffffffffu, ns, 31);
+            for (int i = 0; i < n; ++i) {
+                MoeProblem pb;
+                pb.expert = (int16_t)id;
+                pb.start = (int16_t)((mine & 0xffff) + i * kMoeChunk);
+                pb.count = (int16_t)min(c - i * kMoeChunk, kMoeChunk);
+                sm.prob[(mine >> 16) + i] = pb;
+            }
+            if (lane == 0) sm.nprob = total >> 16;
         }
-        if (lane == 0) sm.nprob = np;
-    }
-    __syncthreads();
+        __syncthreads();
+    } else {
+        // Pairs by expert, in order (every CTA must come to the same grouping).  Warps
+        // rank the pairs of 32 at a time among those of the same expert and count them;
+        // a thread per expert turns its counts into offsets.
+        const int nch = (P + 31) / 32;
+        uint16_t *counts = reinterpret_cast<uint16_t *>(dyn);  // [nch][E]
+        for (int i = threadIdx.x; i < nch * a.E; i += kMoeThreads) counts[i] = 0;
+        __syncthreads();
+        int id_of[2] = {-1, -1}, rank[2] = {0, 0};  // chunks warp and warp + 16
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const int ch = warp + kMoeWarps * c;
-        if (id_of[c] >= 0) sm.sorted[sm.first[id_of[c]] + counts[ch * a.E + id_of[c]] + rank[c]] = (int16_t)(32 * ch + lane);
+        for (int c = 0; c < 2; ++c) {
+            const int ch = warp + kMoeWarps * c, p = 32 * ch + lane;
+            if (ch >= nch) break;
+            const int id = p < P ? sm.ids[p] : -1;
+            const uint32_t same = __match_any_sync(0xffffffffu, id);
+            id_of[c] = id;
+            rank[c] = __popc(same & ((1u << lane) - 1u));
+            if (id >= 0 && rank[c] == 0) counts[ch * a.E + id] = (uint16_t)__popc(same);
+        }
+        __syncthreads();
+        if ((int)threadIdx.x < a.E) {
+            int n = 0;
+            for (int ch = 0; ch < nch; ++ch) {
+                const int c = counts[ch * a.E + threadIdx.x];
+                counts[ch * a.E + threadIdx.x] = (uint16_t)n;
+                n += c;
+            }
+            sm.count[threadIdx.x] = (int16_t)n;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            int at = 0, np = 0;  // running sums over experts
+            for (int e0 = 0; e0 < a.E; e0 += 32) {
+                const int e = e0 + lane;
+                const int c = e < a.E ? sm.count[e] : 0, n = (c + kMoeChunk - 1) / kMoeChunk;
+                int cs = c, ns = n;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int v = __shfl_up_sync(0xffffffffu, cs, off), u = __shfl_up_sync(0xffffffffu, ns, off);
+                    if (lane >= off) {
+                        cs += v;
+                        ns += u;
+                    }
+                }
+                if (e < a.E) {
+                    sm.first[e] = (int16_t)(at + cs - c);
+                    for (int i = 0; i < n; ++i) {
+                        MoeProblem pb;
+                        pb.expert = (int16_t)e;
+                        pb.start = (int16_t)(at + cs - c + i * kMoeChunk);
+                        pb.count = (int16_t)(c - i * kMoeChunk < kMoeChunk ? c - i * kMoeChunk : kMoeChunk);
+                        sm.prob[np + ns - n + i] = pb;
+                    }
+                }
+                at += __shfl_sync(0xffffffffu, cs, 31);
+                np += __shfl_sync(0xffffffffu, ns, 31);
+            }
+            if (lane == 0) sm.nprob = np;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int ch = warp + kMoeWarps * c;
+            if (id_of[c] >= 0) sm.sorted[sm.first[id_of[c]] + counts[ch * a.E + id_of[c]] + rank[c]] = (int16_t)(32 * ch + lane);
+        }
+        __syncthreads();
     }
-    __syncthreads();
 
     // ---------------- gate, up, activation ----------------
     int *red = reinterpret_cast<int *>(dyn);
@@ -707,7 +846,13 @@ __global__ void __launch_bounds__(kMoeThreads, 1) tq_moe_experts_kernel(const __
         moe_contract<true, CONV, PD>(a, sm, run, ring, x_s, red);
     }
     MoeRun run = moe_run<false>(a, sm);
-    for (int p = 0; p < PD; ++p) moe_load<false>(a, sm, run, ring + 2048u * p);  // on their way during the rotation
+    const bool joint = FEW && moe_run_joint(a, sm, run);
+    for (int p = 0; p < PD; ++p) {  // on their way during the rotation
+        if (FEW && joint)
+            moe_load<false, true>(a, sm, run, ring + 2048u * p);
+        else
+            moe_load<false>(a, sm, run, ring + 2048u * p);
+    }
     if (!moe_grid_sync(a.barrier, ++phase, &sm.flag)) {
         cp_async_wait_groups<0>();
         return;
@@ -732,6 +877,10 @@ __global__ void __launch_bounds__(kMoeThreads, 1) tq_moe_experts_kernel(const __
         return;
     }
     // ---------------- down ----------------
+    if (FEW && joint) {
+        moe_down_joint<CONV, PD>(a, sm, run, ring, x_s, red);
+        return;
+    }
     moe_contract<false, CONV, PD>(a, sm, run, ring, x_s, red);
     if (!moe_grid_sync(a.barrier, ++phase, &sm.flag)) return;
     // ---------------- sum over the slots ----------------

@@ -137,6 +137,31 @@ def test_layer(cuda_lib, M, D, F, E, k, per_row, rms, norm):
     assert torch.equal(y, y2)
 
 
+# Up to 16 pairs: each of 16 a problem, one expert with all of them, between, one more.
+FEW = [(2, 512, 512, 64, 8), (16, 1024, 512, 1, 1), (16, 1536, 2048, 2, 1), (8, 2048, 1536, 8, 2), (2, 8192, 8192, 8, 8),
+       (1, 2048, 1024, 64, 16), (5, 1024, 4608, 3, 3), (1, 512, 8192, 40, 9), (17, 1024, 512, 4, 1)]
+
+
+@pytest.mark.parametrize("M,D,F,E,k", FEW)
+def test_few_pairs(cuda_lib, M, D, F, E, k):
+    tq = cuda_lib
+    x, router, layers = make(M + D + F + E + k, M, D, F, E, True)
+    y, ids, w = tq.moe_swiglu(x, router, *layers, k, per_row=True)
+    ref, mag, rid, rw = reference(x, router, layers, k, True, True, True, 0)
+    assert tq.device_status() == 0
+    assert torch.equal(ids.long(), rid)
+    check_y(y, ref, mag, k)
+    # every other pair without an expert, then all
+    for drop in (slice(1, None, 2), slice(None)):
+        ids.view(-1)[drop] = -1
+        ref, mag, _, _ = reference(x, None, layers, k, True, True, True, 0, ids=ids.long(), w=w)
+        fl = tq.FLAG_FWHT | tq.FLAG_RMSNORM | tq.GAMMA_PER_ROW
+        y = torch.full_like(x, float("nan"))
+        ws = torch.empty(tq.moe_workspace_bytes(M, D, F, E, k, fl), dtype=torch.uint8, device="cuda")
+        tq.moe_swiglu_(x, None, *layers, fl, y, ids, w, ws)
+        check_y(y, ref, mag, k)
+
+
 @pytest.mark.parametrize("enc", [1, 2])
 @pytest.mark.parametrize("M", [2, 40])
 def test_layouts(cuda_lib, M, enc):
