@@ -1437,6 +1437,9 @@ tq_status tq_moe_swiglu(const float *x, int64_t M, int64_t d_model, int64_t d_ff
     a.k = (int)top_k;
     a.inv_d = 1.0 / (double)d_model;
     a.inv_f = 1.0 / (double)d_ffn;
+    a.by_grid = ((1ull << 36) + sms - 1) / sms;
+    a.by_gate = (uint32_t)(((1ull << 32) + d_ffn / 16 - 1) / (d_ffn / 16));
+    a.by_down = (uint32_t)(((1ull << 32) + d_model / 32 - 1) / (d_model / 32));
     a.per_row = pr ? 1 : 0;
     a.norm_topk = (flags & TQ_FLAG_NORM_TOPK) ? 1 : 0;
     a.enc = enc;

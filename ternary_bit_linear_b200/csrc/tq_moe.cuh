@@ -76,6 +76,10 @@ struct MoeArgs {
     int M, D, F, E, k;
     int per_row, norm_topk, enc;
     double inv_d, inv_f;  // 1 / D, 1 / F
+    // Quotients by the number of CTAs n (of less than 2^36 / n) and by a problem's
+    // strips (of less than 2^32 / strips): ceil(2^36 / n), ceil(2^32 / strips).
+    uint64_t by_grid;
+    uint32_t by_gate, by_down;
     float clamp_val;
     ActParams act;
     // workspace
@@ -359,35 +363,58 @@ struct MoeShared {
 // This CTA's share of a contraction phase: a run of consecutive strips of all
 // problems' strips.  GATE: a strip is rows n0 .. n0 + 15 of gate and up, giving
 // activations; else rows n0 .. n0 + 31 of down, giving outputs.  Teams of ks warps
-// share a strip's column steps, as many as keep every warp busy when runs are short.
+// share a strip's column steps, where the run's strips would leave warps without
+// work in its last rounds.
 struct MoeRun {
     int s0, s1;
-    int ks, team, kw;  // warps per strip; this warp's team and place in it
+    int lg, ks, team, kw;  // ks = 2^lg warps per strip; this warp's team and place in it
     int mine;          // its column steps kw, kw + ks, ... of a strip
     int spp;           // strips per problem
     // the next step to request: problem, strip, step; strips of that problem end at `end`
     int q, strip, end, i;
 };
 
+__device__ __forceinline__ void moe_team(MoeRun &r, int lg, int steps) {
+    const int warp = threadIdx.x >> 5;
+    r.lg = lg;
+    r.ks = 1 << lg;
+    r.team = warp >> lg;
+    r.kw = warp & (r.ks - 1);
+    r.mine = (steps - r.kw + r.ks - 1) >> lg;
+    r.i = 0;
+}
+
 template <bool GATE>
 __device__ __forceinline__ MoeRun moe_run(const MoeArgs &a, const MoeShared &sm) {
     MoeRun r;
     r.spp = GATE ? a.F / 16 : a.D / 32;
-    const int total = sm.nprob * r.spp;  // at most 384 x 512
-    const int n = (int)gridDim.x, b = (int)blockIdx.x, steps = (GATE ? a.D : a.F) / 256;
-    r.s0 = (int)((unsigned)(total * b) / (unsigned)n);
-    r.s1 = (int)((unsigned)(total * (b + 1)) / (unsigned)n);
-    const int run = (total + n - 1) / n;
-    r.ks = kMoeWarps;
-    while (r.ks > 1 && (kMoeWarps / r.ks < run || r.ks > steps)) r.ks >>= 1;
-    const int warp = threadIdx.x >> 5;
-    r.team = warp / r.ks;
-    r.kw = warp % r.ks;
-    r.mine = (steps - r.kw + r.ks - 1) / r.ks;
-    r.q = r.s0 / r.spp;
+    const unsigned total = sm.nprob * r.spp, b = blockIdx.x;  // at most 384 x 512 strips
+    const int steps = (GATE ? a.D : a.F) / 256;
+    r.s0 = (int)((total * b) * a.by_grid >> 36);
+    r.s1 = (int)((total * (b + 1)) * a.by_grid >> 36);
+    const unsigned by = GATE ? a.by_gate : a.by_down;
+    r.q = (int)__umulhi((unsigned)r.s0, by);
+    // the run's strips in its first problem, whole problems, strips in the last one
+    const int first = min(r.s1 - r.s0, (r.q + 1) * r.spp - r.s0), rest = r.s1 - r.s0 - first;
+    const int whole = (int)__umulhi((unsigned)rest, by), last = rest - whole * r.spp;
+    // A round of all teams takes a strip's steps, shared, and with more than one warp
+    // the exchange of sums, about two steps.  64 tokens of 1536 x 6144, 8 experts:
+    // 60.2 us, 61.6 us with one warp per strip; 2 of 7168 x 2048, 8 of 256: 68.7 to
+    // 80.5 us; without the exchange's term 64 of 2048 x 1536, 8 of 128: 159 to 97 us.
+    int best = 0, least = 0x7fffffff;
+#pragma unroll
+    for (int lg = 0; lg <= 4; ++lg) {
+        const int up = (kMoeWarps >> lg) - 1, down = 4 - lg;
+        const int rounds = ((first + up) >> down) + whole * ((r.spp + up) >> down) + ((last + up) >> down);
+        const int cost = rounds * (((steps + (1 << lg) - 1) >> lg) + (lg > 0 ? 2 : 0));
+        if (cost < least && (1 << lg) <= steps) {
+            least = cost;
+            best = lg;
+        }
+    }
+    moe_team(r, best, steps);
     r.strip = r.s0 - r.q * r.spp + r.team;
     r.end = min(r.s1 - r.q * r.spp, r.spp);
-    r.i = 0;
     return r;
 }
 
@@ -398,20 +425,23 @@ __device__ __forceinline__ MoeRun moe_run(const MoeArgs &a, const MoeShared &sm)
 // `r` is the other form's run, and becomes this one's.
 __device__ __forceinline__ bool moe_run_joint(const MoeArgs &a, const MoeShared &sm, MoeRun &r) {
     if (sm.nprob == 0) return false;
-    const int steps = a.F / 256, n = (int)gridDim.x, warp = threadIdx.x >> 5;
-    int ks = kMoeWarps;
-    while (ks > 1 && (kMoeWarps / ks < sm.nprob || ks > steps)) ks >>= 1;
-    const int T = kMoeWarps / r.ks, run = (sm.nprob * r.spp + n - 1) / n;
-    if ((r.spp + n - 1) / n * ((steps + ks - 1) / ks) > (run + T - 1) / T * ((steps + r.ks - 1) / r.ks) + 4) return false;
-    r.ks = ks;
-    r.team = warp / r.ks;
-    r.kw = warp % r.ks;
-    r.mine = (steps - r.kw + r.ks - 1) / r.ks;
+    const int steps = a.F / 256, n = (int)gridDim.x;
+    int mine = 4;
+    while (mine > 0 && ((kMoeWarps >> mine) < sm.nprob || (1 << mine) > steps)) --mine;
+    // the other form's, for the longest run (every CTA must come to the same form)
+    const auto over_grid = [&](int v) { return (int)((unsigned)(v + n - 1) * a.by_grid >> 36); };
+    const int run = over_grid(sm.nprob * r.spp);
+    int apart = 0x7fffffff;
+#pragma unroll
+    for (int lg = 0; lg <= 4; ++lg)
+        if ((1 << lg) <= steps)
+            apart = min(apart, ((run + (kMoeWarps >> lg) - 1) >> (4 - lg)) * ((steps + (1 << lg) - 1) >> lg));
+    if (over_grid(r.spp) * ((steps + (1 << mine) - 1) >> mine) > apart + 4) return false;
+    moe_team(r, mine, steps);
     r.q = r.team;
     r.s1 = (r.q + 1) * r.spp;
     r.strip = (int)blockIdx.x;
     r.end = r.team < sm.nprob ? r.spp : 0;
-    r.i = 0;
     return true;
 }
 
@@ -436,7 +466,7 @@ __device__ __forceinline__ void moe_load(const MoeArgs &a, const MoeShared &sm, 
         cp_async16(slot + 1536, q + 8 * KB);
         if (++r.i == r.mine) {
             r.i = 0;
-            r.strip += JOINT ? (int)gridDim.x : kMoeWarps / r.ks;
+            r.strip += JOINT ? (int)gridDim.x : kMoeWarps >> r.lg;
         }
     }
     cp_async_commit();
@@ -516,19 +546,20 @@ template <bool GATE, bool CONV, int PD>
 __device__ __forceinline__ void moe_contract(const MoeArgs &a, const MoeShared &sm, MoeRun &run, uint32_t ring, uint32_t x_s,
                                              int *red) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int ks = run.ks, team = run.team, kw = run.kw, T = kMoeWarps / ks, spp = run.spp;
+    const int ks = run.ks, team = run.team, kw = run.kw, T = kMoeWarps >> run.lg, spp = run.spp;
     const int g = lane >> 2, t = lane & 3;
     const int K = GATE ? a.D : a.F, N = GATE ? a.F : a.D, XS = gemv_x_stride(K);
     const uint32_t xsw = (uint32_t)(t & 2) << 4;
     float *val = reinterpret_cast<float *>(red + warp * kMoeSlot);
     if (run.s0 >= run.s1) return;
     int buf = 0;
-    moe_stage<GATE>(a, sm, sm.prob[run.s0 / spp], x_s);
+    const int q0 = (int)__umulhi((unsigned)run.s0, GATE ? a.by_gate : a.by_down);
+    moe_stage<GATE>(a, sm, sm.prob[q0], x_s);
     cp_async_commit();
     cp_async_wait_groups<0>();
     __syncthreads();
     int slot = 0;
-    for (int at = run.s0, q = run.s0 / spp; at < run.s1; ++q) {
+    for (int at = run.s0, q = q0; at < run.s1; ++q) {
         const int first = q * spp, end = min(run.s1, first + spp);
         const MoeProblem pb = sm.prob[q];
         const bool more = end < run.s1;
