@@ -1438,6 +1438,12 @@ tq_status tq_moe_swiglu(const float *x, int64_t M, int64_t d_model, int64_t d_ff
     a.inv_d = 1.0 / (double)d_model;
     a.inv_f = 1.0 / (double)d_ffn;
     a.by_grid = ((1ull << 36) + sms - 1) / sms;
+    a.by_d = (uint32_t)(((1ull << 32) + d_model / 16 - 1) / (d_model / 16));
+    a.by_f = (uint32_t)(((1ull << 32) + d_ffn / 16 - 1) / (d_ffn / 16));
+    a.by_k = (uint32_t)((65536 + top_k - 1) / top_k);
+    const uint32_t groups = (uint32_t)((M + kMoeRouteTokens - 1) / kMoeRouteTokens);
+    a.by_groups = (65536 + groups - 1) / groups;
+    a.by_warps = (uint32_t)((256 + d_ffn / 512 - 1) / (d_ffn / 512));
     a.by_gate = (uint32_t)(((1ull << 32) + d_ffn / 16 - 1) / (d_ffn / 16));
     a.by_down = (uint32_t)(((1ull << 32) + d_model / 32 - 1) / (d_model / 32));
     a.per_row = pr ? 1 : 0;
@@ -1460,7 +1466,7 @@ tq_status tq_moe_swiglu(const float *x, int64_t M, int64_t d_model, int64_t d_ff
     a.rh = reinterpret_cast<int32_t *>(ws + off[8]);
     a.out = reinterpret_cast<float *>(ws + off[9]);
     cudaStream_t st = cs(stream);
-    const int64_t units = router ? (n_experts + kMoeRouteExperts - 1) / kMoeRouteExperts * ((M + kMoeRouteTokens - 1) / kMoeRouteTokens) : 0;
+    const int64_t units = router ? (n_experts + kMoeRouteExperts - 1) / kMoeRouteExperts * groups : 0;
     if (tq_status e = launch_pdl(tq_moe_route_kernel, dim3((unsigned)(M + units)), dim3(kMoeThreads), 0, st, a)) return e;
     if (d_model <= kMoeRingK && d_ffn <= kMoeRingK)
         return enc != kEncFoundry ? launch_moe_experts<true, 4>(a, sms, st) : launch_moe_experts<false, 4>(a, sms, st);

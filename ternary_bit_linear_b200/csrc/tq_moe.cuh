@@ -80,6 +80,9 @@ struct MoeArgs {
     // strips (of less than 2^32 / strips): ceil(2^36 / n), ceil(2^32 / strips).
     uint64_t by_grid;
     uint32_t by_gate, by_down;
+    uint32_t by_d, by_f;       // the same for the 16-byte chunks of a token row, D / 16 and F / 16
+    uint32_t by_k, by_groups;  // ceil(2^16 / k), ceil(2^16 / the route kernel's groups of tokens)
+    uint32_t by_warps;         // ceil(2^8 / (F / 512))
     float clamp_val;
     ActParams act;
     // workspace
@@ -212,7 +215,8 @@ __global__ void __launch_bounds__(kMoeThreads, 2) tq_moe_route_kernel(const __gr
         return;
     }
     const int u = blockIdx.x - a.M, tgroups = (a.M + kMoeRouteTokens - 1) / kMoeRouteTokens;
-    const int e0 = u / tgroups * kMoeRouteExperts + (warp >> 2) * 2, m0 = u % tgroups * kMoeRouteTokens;
+    const int eg = (int)((unsigned)u * a.by_groups >> 16);
+    const int e0 = eg * kMoeRouteExperts + (warp >> 2) * 2, m0 = (u - eg * tgroups) * kMoeRouteTokens;
     const int nt = a.M - m0 < kMoeRouteTokens ? a.M - m0 : kMoeRouteTokens;
     const int nv = a.D / 4, q0 = (warp & 3) * (nv / 4);  // float4; a quarter is a multiple of 32
     const float4 *wr[2];
@@ -256,7 +260,7 @@ __global__ void __launch_bounds__(kMoeThreads, 2) tq_moe_route_kernel(const __gr
     }
     __syncthreads();
     if (threadIdx.x < kMoeRouteExperts * nt) {
-        const int t = threadIdx.x / kMoeRouteExperts, i = threadIdx.x % kMoeRouteExperts, e = u / tgroups * kMoeRouteExperts + i;
+        const int t = threadIdx.x / kMoeRouteExperts, i = threadIdx.x % kMoeRouteExperts, e = eg * kMoeRouteExperts + i;
         double v = 0.0;
 #pragma unroll
         for (int q = 0; q < 4; ++q) v = __dadd_rn(v, part[(i >> 1) * 4 + q][2 * t + (i & 1)]);
@@ -472,14 +476,16 @@ __device__ __forceinline__ void moe_load(const MoeArgs &a, const MoeShared &sm, 
     cp_async_commit();
 }
 
+__device__ __forceinline__ int moe_token(const MoeArgs &a, int p) { return (int)((unsigned)p * a.by_k >> 16); }  // p / k
+
 // A problem's token codes into shared memory (not committed).
 template <bool GATE>
 __device__ __forceinline__ void moe_stage(const MoeArgs &a, const MoeShared &sm, const MoeProblem &pb, uint32_t x_s) {
     const int K = GATE ? a.D : a.F, XS = gemv_x_stride(K), cpr = K >> 4;
     for (int i = threadIdx.x; i < pb.count * cpr; i += kMoeThreads) {
-        const int r = i / cpr, c = i - r * cpr;
+        const int r = (int)__umulhi((unsigned)i, GATE ? a.by_d : a.by_f), c = i - r * cpr;
         const int p = sm.sorted[pb.start + r];
-        cp_async16(x_s + (uint32_t)(r * XS + 16 * c), (GATE ? a.xq + (int64_t)(p / a.k) * K : a.hq + (int64_t)p * K) + 16 * c);
+        cp_async16(x_s + (uint32_t)(r * XS + 16 * c), (GATE ? a.xq + (int64_t)moe_token(a, p) * K : a.hq + (int64_t)p * K) + 16 * c);
     }
 }
 
@@ -539,6 +545,23 @@ __device__ __forceinline__ void moe_values(float *val, const int (&acc)[2][4], c
         }
 }
 
+// Token m's weights, by one warp.  mine: the logit of slot `lane`; top: the largest.
+__device__ __forceinline__ void moe_weights(const MoeArgs &a, MoeShared &sm, int m, float mine, float top) {
+    const int lane = threadIdx.x & 31;
+    const double ex = lane < a.k ? exp((double)mine - (double)top) : 0.0;
+    double den = ex;
+    if (!a.norm_topk) {
+        den = 0.0;
+        for (int e = lane; e < a.E; e += 32) den = __dadd_rn(den, exp((double)__ldcg(a.logits + (int64_t)m * a.E + e) - (double)top));
+    }
+    den = warp_sum_d(den);
+    if (lane < a.k) {
+        const float w = __double2float_rn(__ddiv_rn(ex, den));
+        sm.w[m * a.k + lane] = w;
+        if (a.M > kMoeWarps || blockIdx.x == 0) a.weights[m * a.k + lane] = w;
+    }
+}
+
 // The run, the first PD steps of each warp requested before.  While a problem's
 // strips are contracted, the next one's codes are copied to the other buffer; the
 // ring goes on from strip to strip and problem to problem.
@@ -571,7 +594,7 @@ __device__ __forceinline__ void moe_contract(const MoeArgs &a, const MoeShared &
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int i = 2 * t + e < pb.count ? 2 * t + e : 0;
-            const int p = sm.sorted[pb.start + i], src = GATE ? p / a.k : p;
+            const int p = sm.sorted[pb.start + i], src = GATE ? moe_token(a, p) : p;
             sv[e] = __ldcg((GATE ? a.sx : a.sh) + src);
             rv[e] = __ldcg((GATE ? a.rs : a.rh) + src);
         }
@@ -631,7 +654,7 @@ __device__ __forceinline__ void moe_down_joint(const MoeArgs &a, const MoeShared
     const MoeProblem last = sm.prob[sm.nprob - 1];
     // every pair's codes, at most 16 rows (the two buffers' room), in sorted order
     for (int i = threadIdx.x; i < (last.start + last.count) * cpr; i += kMoeThreads) {
-        const int r = i / cpr, c = i - r * cpr;
+        const int r = (int)__umulhi((unsigned)i, a.by_f), c = i - r * cpr;
         cp_async16(x_s + (uint32_t)(r * XS + 16 * c), a.hq + (int64_t)sm.sorted[r] * K + 16 * c);
     }
     cp_async_commit();
@@ -697,6 +720,7 @@ __global__ void __launch_bounds__(kMoeThreads, 1) tq_moe_experts_kernel(const __
     // Up to 16 tokens, a warp of every CTA for each; more, a CTA for each, and the
     // others read its choice after a barrier.
     const bool spread = a.router && a.M > kMoeWarps;
+    float slot_logit = 0.0f, top_logit = 0.0f;
     for (int m = spread ? (int)blockIdx.x : warp; m < a.M; m += spread ? (int)gridDim.x : kMoeWarps) {
         if (!a.router || (spread && warp != 0)) break;
         constexpr int V = kMoeMaxExperts / 32;
@@ -741,26 +765,13 @@ __global__ void __launch_bounds__(kMoeThreads, 1) tq_moe_experts_kernel(const __
                 scan();
             }
         }
-        double den;
-        const double ex = lane < a.k ? exp((double)mine - (double)top) : 0.0;
-        if (a.norm_topk) {
-            den = warp_sum_d(ex);
-        } else {
-            den = 0.0;
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (lane + 32 * i < a.E) den = __dadd_rn(den, exp((double)l[i] - (double)top));
-            den = warp_sum_d(den);
-        }
         if (lane < a.k) {
-            const float w = __double2float_rn(__ddiv_rn(ex, den));
             sm.ids[m * a.k + lane] = my_id;
-            sm.w[m * a.k + lane] = w;
-            if (spread || blockIdx.x == 0) {
-                a.ids[m * a.k + lane] = my_id;
-                a.weights[m * a.k + lane] = w;
-            }
+            if (spread || blockIdx.x == 0) a.ids[m * a.k + lane] = my_id;
         }
+        if (spread) moe_weights(a, sm, m, mine, top);
+        slot_logit = mine;
+        top_logit = top;
     }
     if (spread && !moe_grid_sync(a.barrier, ++phase, &sm.flag)) return;
     if (!a.router || spread)
@@ -874,6 +885,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) tq_moe_experts_kernel(const __
     {
         MoeRun run = moe_run<true>(a, sm);
         for (int p = 0; p < PD; ++p) moe_load<true>(a, sm, run, ring + 2048u * p);
+        // the weights are wanted at the end: while the first loads are on their way
+        if (a.router && !spread && warp < a.M) moe_weights(a, sm, warp, slot_logit, top_logit);
         moe_contract<true, CONV, PD>(a, sm, run, ring, x_s, red);
     }
     MoeRun run = moe_run<false>(a, sm);
@@ -890,8 +903,8 @@ __global__ void __launch_bounds__(kMoeThreads, 1) tq_moe_experts_kernel(const __
     }
     // ---------------- rotation and codes of every pair ----------------
     {
-        const int nw = a.F / 512, fit = kMoeWarps / nw, teams = fit < 15 ? fit : 15;  // named barriers 1 .. 15
-        const int team = warp / nw, wt = warp % nw;
+        const int nw = a.F / 512, fit = (int)(kMoeWarps * a.by_warps >> 8), teams = fit < 15 ? fit : 15;  // named barriers 1 .. 15
+        const int team = (int)((unsigned)warp * a.by_warps >> 8), wt = warp - team * nw;
         if (team < teams) {
             for (int p = (int)blockIdx.x + team * (int)gridDim.x; p < P; p += teams * (int)gridDim.x) {
                 if (sm.ids[p] < 0) continue;
