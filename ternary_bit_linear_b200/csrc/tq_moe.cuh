@@ -21,9 +21,10 @@
 //     logits of 8 experts and four tokens each.
 //   tq_moe_experts_kernel: one CTA per SM, launched cooperatively (all CTAs
 //     resident), with grid-wide barriers between its phases:
-//       choice     every CTA picks every token's experts (for up to 16 tokens that is
-//                  cheaper than another barrier) and sorts the (token, slot) pairs by expert; an expert
-//                  and up to 8 of its pairs are one "problem".
+//       choice     every CTA picks every token's experts (for up to 16 tokens that
+//                  is cheaper than another barrier) and sorts the (token, slot)
+//                  pairs by expert; an expert and up to 8 of its pairs are one
+//                  "problem".
 //       gate, up   a strip is 16 rows of both matrices, so that the activation
 //                  follows in registers.  The strips of all problems are split
 //                  into contiguous runs, one per CTA; the quantised tokens of a
@@ -34,7 +35,7 @@
 //                  the result does not depend on how pairs were grouped.
 //       For up to 16 pairs, where it costs few steps more, a CTA contracts a strip
 //       of down for every pair at once and adds them itself: down and sum without
-//       the barrier between them (one token of 512 x 1024: 16.9 us, 18.9 us apart).
+//       the barrier between them (about 2 us).
 //   A warp streams its strips' weights from HBM by asynchronous copies into a ring
 //   of its own, two or four column steps (of 2 KB) ahead, across strips and problems,
 //   and into the down phase from before the rotation; a lane reads only what it
@@ -360,6 +361,8 @@ struct MoeShared {
     int16_t count[kMoeMaxExperts], first[kMoeMaxExperts];
     MoeProblem prob[kMoeMaxProblems];
     int16_t where[kMoeFew];  // of up to so many pairs: problem << 8 | place in it
+    float few_s[kMoeFew];    // the scales and sums of codes that a CTA computes itself
+    int few_r[kMoeFew];
     int nprob, flag;
     MoeRed red;
 };
@@ -648,30 +651,34 @@ __device__ __forceinline__ void moe_contract(const MoeArgs &a, const MoeShared &
 // The down phase with its sum (moe_run_joint), the first steps requested before.
 template <bool CONV, int PD>
 __device__ __forceinline__ void moe_down_joint(const MoeArgs &a, const MoeShared &sm, MoeRun &run, uint32_t ring, uint32_t x_s,
-                                               int *red) {
+                                               int *red, bool here) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int K = a.F, XS = gemv_x_stride(K), cpr = K >> 4;
     const MoeProblem last = sm.prob[sm.nprob - 1];
     // every pair's codes, at most 16 rows (the two buffers' room), in sorted order
-    for (int i = threadIdx.x; i < (last.start + last.count) * cpr; i += kMoeThreads) {
-        const int r = (int)__umulhi((unsigned)i, a.by_f), c = i - r * cpr;
-        cp_async16(x_s + (uint32_t)(r * XS + 16 * c), a.hq + (int64_t)sm.sorted[r] * K + 16 * c);
+    if (!here) {
+        for (int i = threadIdx.x; i < (last.start + last.count) * cpr; i += kMoeThreads) {
+            const int r = (int)__umulhi((unsigned)i, a.by_f), c = i - r * cpr;
+            cp_async16(x_s + (uint32_t)(r * XS + 16 * c), a.hq + (int64_t)sm.sorted[r] * K + 16 * c);
+        }
+        cp_async_commit();
     }
-    cp_async_commit();
     const bool active = run.team < sm.nprob;
     const MoeProblem pb = sm.prob[active ? run.team : 0];
     float sv[2];
     int rv[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        const int p = sm.sorted[pb.start + min(2 * t + e, pb.count - 1)];
-        sv[e] = __ldcg(a.sh + p);
-        rv[e] = __ldcg(a.rh + p);
+        const int i = pb.start + min(2 * t + e, pb.count - 1), p = sm.sorted[i];
+        sv[e] = here ? sm.few_s[i] : __ldcg(a.sh + p);
+        rv[e] = here ? sm.few_r[i] : __ldcg(a.rh + p);
     }
     const uint32_t xr = x_s + (uint32_t)((pb.start + min(g, pb.count - 1)) * XS + 64 * t + 256 * run.kw);
     const uint32_t xsw = (uint32_t)(t & 2) << 4;
-    cp_async_wait_groups<0>();
-    __syncthreads();
+    if (!here) {
+        cp_async_wait_groups<0>();
+        __syncthreads();
+    }
     int slot = 0;
     for (int s = (int)blockIdx.x; s < run.spp; s += (int)gridDim.x) {
         const int n0 = 32 * s;
@@ -902,27 +909,44 @@ __global__ void __launch_bounds__(kMoeThreads, 1) tq_moe_experts_kernel(const __
         return;
     }
     // ---------------- rotation and codes of every pair ----------------
+    // Where a CTA's teams do all pairs in one round (and the down phase reads them
+    // all), every CTA does, straight into its shared memory, without a barrier after
+    // it: one token of 512 x 1024 14.6 us, 16.1 us with each pair in one CTA.  Two
+    // rounds cost more than the barrier (one of 1536 x 6144: 21.8 us to 20.4 us).
+    bool here = false;
+    int rows = 0;
     {
         const int nw = a.F / 512, fit = (int)(kMoeWarps * a.by_warps >> 8), teams = fit < 15 ? fit : 15;  // named barriers 1 .. 15
         const int team = (int)((unsigned)warp * a.by_warps >> 8), wt = warp - team * nw;
+        if (FEW && joint) {
+            const MoeProblem pb = sm.prob[sm.nprob - 1];
+            rows = pb.start + pb.count;
+            here = rows <= teams;
+        }
         if (team < teams) {
-            for (int p = (int)blockIdx.x + team * (int)gridDim.x; p < P; p += teams * (int)gridDim.x) {
+            const int n = FEW && here ? 1 : (int)gridDim.x, end = FEW && here ? rows : P;
+            for (int j = (FEW && here ? 0 : (int)blockIdx.x) + team * n; j < end; j += teams * n) {
+                const int p = FEW && here ? sm.sorted[j] : j;
                 if (sm.ids[p] < 0) continue;
                 float f[16];
                 load_block16(f, a.h + (int64_t)p * a.F, wt);
-                moe_rot_quant(f, wt, nw, 1 + team, a.act, a.inv_f, a.hq + (int64_t)p * a.F, a.sh + p, a.rh + p,
-                              sm.red.f + team * nw, sm.red.i + team * nw, sm.red.d + team * nw);
+                int8_t *dst = FEW && here ? reinterpret_cast<int8_t *>(dyn + kMoeRedBytes + kMoeWarps * PD * 2048) + j * gemv_x_stride(a.F)
+                                          : a.hq + (int64_t)p * a.F;
+                moe_rot_quant(f, wt, nw, 1 + team, a.act, a.inv_f, dst, FEW && here ? sm.few_s + j : a.sh + p,
+                              FEW && here ? sm.few_r + j : a.rh + p, sm.red.f + team * nw, sm.red.i + team * nw, sm.red.d + team * nw);
                 bar_sync_n(1 + team, 32 * nw);  // the slots of red are written again
             }
         }
     }
-    if (!moe_grid_sync(a.barrier, ++phase, &sm.flag)) {
+    if (FEW && here) {
+        __syncthreads();
+    } else if (!moe_grid_sync(a.barrier, ++phase, &sm.flag)) {
         cp_async_wait_groups<0>();
         return;
     }
     // ---------------- down ----------------
     if (FEW && joint) {
-        moe_down_joint<CONV, PD>(a, sm, run, ring, x_s, red);
+        moe_down_joint<CONV, PD>(a, sm, run, ring, x_s, red, here);
         return;
     }
     moe_contract<false, CONV, PD>(a, sm, run, ring, x_s, red);
