@@ -98,7 +98,8 @@ __device__ __forceinline__ float4 fp8_load4(const void *x, int64_t row, int64_t 
 // ---------------------------------------------------------------------------
 // 1 x 128 blocks.  One warp takes 512 columns of one row: four blocks, each of
 // its lanes four consecutive elements of each, so a block's maximum is one
-// warp reduction and its 128 codes one coalesced store.
+// warp reduction and its 128 codes one coalesced store.  11008 x 4096 fp32:
+// 36.6 us, 6.2 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kFp8RowWarps = 8;
 
@@ -181,7 +182,10 @@ __global__ void __launch_bounds__(kActThreads)
 // lane l the columns 4 l .. 4 l + 3: a row's maximum is a warp reduction, a
 // column's meets in shared memory, and a thread's 16 rows of one column are
 // 16 consecutive bytes of the transposed codes, which pass through shared
-// memory to leave in whole 128-byte rows.
+// memory to leave in whole 128-byte rows.  Three tiles per SM, so that one's loads
+// run while another's maxima meet.  11008 x 4096 fp32 to 128 x 128 blocks: 43.6 us,
+// with the transpose 44.9 us (6.0 TB/s); rows and columns, whose scales differ,
+// 60.6 us, each code twice from its own quotient.
 // ---------------------------------------------------------------------------
 template <bool BF16, bool VEC, bool SQUARE, bool TRANS>
 __global__ void __launch_bounds__(256, 3)
