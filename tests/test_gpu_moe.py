@@ -349,3 +349,31 @@ def test_weights_past_32_bit_offsets(cuda_lib):
     ref, mag, _, _ = reference(x, None, small, k, True, True, True, 0, ids=near, w=w)
     check_y(y, ref, mag, k)
     assert tq.device_status() == 0
+
+
+@pytest.mark.parametrize("M,D,F,E,k", [(1, 512, 1024, 8, 2), (1, 1536, 6144, 8, 2), (2, 512, 512, 64, 8)])
+def test_few_pairs_repeatable_on_two_streams(cuda_lib, M, D, F, E, k):
+    """Captured steps of a few pairs, replayed side by side: the same bits every time."""
+    tq = cuda_lib
+    x, router, layers = make(7 * D + F, M, D, F, E, False)
+    want, ids, w = tq.moe_swiglu(x, router, *layers, k)
+    fl = tq.FLAG_FWHT | tq.FLAG_RMSNORM | tq.FLAG_NORM_TOPK
+    runs = []
+    for _ in range(2):
+        st, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        out = (torch.empty_like(x), torch.empty_like(ids), torch.empty_like(w),
+               torch.empty(tq.moe_workspace_bytes(M, D, F, E, k, fl), dtype=torch.uint8, device="cuda"))
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=st):
+            tq.moe_swiglu_(x, router, *layers, fl, *out)
+        runs.append((st, g, out))
+    for _ in range(20):
+        for st, g, out in runs:
+            with torch.cuda.stream(st):
+                out[0].fill_(float("nan"))
+                for _ in range(5):
+                    g.replay()
+        torch.cuda.synchronize()
+        for _, _, out in runs:
+            assert torch.equal(out[0], want) and torch.equal(out[1], ids) and torch.equal(out[2], w)
+    assert tq.device_status() == 0
