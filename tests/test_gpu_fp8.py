@@ -292,3 +292,29 @@ def test_past_32_bit_offsets(cuda_lib):
     check_product(y[-300:], av[-300:], bv, K)
     check_product(y[:300, -300:], av[:300], bv[-300:], K)
     assert tq.device_status() == 0
+
+
+def test_quantize_negative_zero(cuda_lib):
+    """-0 / s is -0, and so is a negative value over an infinite scale: the sign stays in the code (0x80)."""
+    tq = cuda_lib
+    x = normal(7, 130, 260)
+    x[1::5, ::2] = -0.0
+    x[3] = -0.0
+    x[:, 9] = -0.0
+    x[8, :128] *= -1e-30                    # below the floor: quotients that round to nothing
+    check_quant(*tq.quantize_fp8(x), x, False)
+    for square in (False, True):
+        q, s, qt, st = tq.quantize_fp8(x, square=square, transpose=True)
+        check_quant(q, s, x, square)
+        check_quant(qt, st, x.t().contiguous(), square)
+    assert (tq.quantize_fp8(x)[0].view(torch.uint8)[3, :260] == 0x80).all()
+    x[4, 3] = float("inf")
+    raw = tq.quantize_fp8(x)[0].view(torch.uint8)[4, :128]
+    want = torch.where(torch.signbit(x[4, :128]), 0x80, 0)
+    assert torch.equal(torch.cat((raw[:3], raw[4:])).long(), torch.cat((want[:3], want[4:])))
+    # RMSNorm of 0 under a negative gain
+    z, g = normal(8, 2, 300), normal(9, 300)
+    z[:, ::3] = 0.0
+    d = z.double()
+    f = (d * (1.0 / torch.sqrt((d * d).sum(1, keepdim=True) / 300 + torch.tensor(1e-6).double().item())) * g.double()).float()
+    check_quant(*tq.quantize_fp8(z, rmsnorm=True, rms_gain=g), f, False)
