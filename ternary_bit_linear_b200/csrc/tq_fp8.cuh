@@ -166,8 +166,9 @@ __global__ void __launch_bounds__(kActThreads)
         float e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+            // past the row zeros stay zeros, whatever r is (infinite or NaN rows)
             const double g = gain && c + i < C ? (double)__ldg(gain + c + i) : 1.0;
-            e[i] = __double2float_rn(__dmul_rn(__dmul_rn((double)e[i], r), g));
+            e[i] = c + i < C ? __double2float_rn(__dmul_rn(__dmul_rn((double)e[i], r), g)) : 0.0f;
         }
         v = make_float4(e[0], e[1], e[2], e[3]);
         const Fp8Scale sc = fp8_block_scale(warp_max(abs_max4(v)));

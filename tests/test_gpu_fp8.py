@@ -318,3 +318,15 @@ def test_quantize_negative_zero(cuda_lib):
     d = z.double()
     f = (d * (1.0 / torch.sqrt((d * d).sum(1, keepdim=True) / 300 + torch.tensor(1e-6).double().item())) * g.double()).float()
     check_quant(*tq.quantize_fp8(z, rmsnorm=True, rms_gain=g), f, False)
+
+
+@pytest.mark.parametrize("C", [1, 130, 1411])
+def test_padding_of_rows_without_a_finite_norm(cuda_lib, C):
+    """A row with a NaN, and an empty row with eps 0 (whose factor is infinite): the bytes past cols stay zero."""
+    tq = cuda_lib
+    x = normal(C, 3, C)
+    x[0, C // 2], x[1] = float("nan"), 0.0
+    q, _ = tq.quantize_fp8(x, rmsnorm=True, rms_eps=0.0)
+    assert not q.view(torch.uint8)[:, C:].any()
+    assert torch.isnan(q[:2, :C].float()).all()
+    assert torch.equal(q[2:].view(torch.uint8), tq.quantize_fp8(x[2:].clone(), rmsnorm=True, rms_eps=0.0)[0].view(torch.uint8))
