@@ -384,6 +384,9 @@ TQ_API size_t tq_swiglu_workspace_bytes(int64_t M, int64_t d_model, int64_t d_ff
  * Every expert quantises the same rotated (and with TQ_FLAG_RMSNORM normalised)
  * token; SiLU(gate) * up is evaluated in fp64 and rounded to fp32 before the
  * clamp and the down projection's own [RMSNorm,] rotation and quantisation.
+ * Without TQ_FLAG_SANITIZE_NONFINITE a NaN or an infinity in a token makes that
+ * token's y NaN (0 if it has no used slot) and no other's; a NaN among an expert's
+ * gammas reaches only the tokens that chose the expert.
  *
  *   x          [M][d_model] fp32.  1 <= M <= 64; d_model, d_ffn multiples of 512,
  *              at most 8192; 1 <= n_experts <= 256; top_k <= 16, n_experts.  For

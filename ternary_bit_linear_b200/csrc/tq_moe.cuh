@@ -146,14 +146,16 @@ __device__ __forceinline__ void moe_rot_quant(float (&f)[16], int wt, int nw, in
         for (int i = 0; i < 16; ++i) f[i] = __double2float_rn(__dmul_rn((double)f[i], r));
     }
     fwht512_regs(f, true);
-    float amax = 0.0f;
+    // Maxima by the values' bits: a NaN's are above all others', makes the scale NaN, and
+    // with it every output of this row.
+    unsigned top = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
-    amax = warp_max_nonneg(amax);
+    for (int i = 0; i < 16; ++i) top = max(top, __float_as_uint(f[i]) & 0x7fffffffu);
+    float amax = warp_max_nonneg(__uint_as_float(top));
     if (lane == 0) redf[wt] = amax;
     bar_sync_n(bar, 32 * nw);
     amax = warp_max_nonneg(lane < nw ? redf[lane] : 0.0f);
-    const float eta = eta_of(amax, p);
+    const float eta = amax != amax ? amax : eta_of(amax, p);
     const float scale = __fdiv_rn(127.0f, eta);
     uint32_t *out = reinterpret_cast<uint32_t *>(dst);
     int sum = 0;
@@ -346,11 +348,11 @@ __device__ __forceinline__ void cp_async_wait_groups() {  // all but the last N 
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// clamp(SiLU(g) u), in fp64, rounded once before the clamp
+// clamp(SiLU(g) u), in fp64, rounded once before the clamp; a NaN stays one
 __device__ __forceinline__ float moe_act(float g, float u, float c) {
     const double gd = (double)g;
     const float v = __double2float_rn(__dmul_rn(__ddiv_rn(gd, __dadd_rn(1.0, exp(-gd))), (double)u));
-    return fminf(fmaxf(v, -c), c);
+    return v != v ? v : fminf(fmaxf(v, -c), c);
 }
 
 // A problem: expert, its pairs sorted[start .. start + count).

@@ -377,3 +377,51 @@ def test_few_pairs_repeatable_on_two_streams(cuda_lib, M, D, F, E, k):
         for _, _, out in runs:
             assert torch.equal(out[0], want) and torch.equal(out[1], ids) and torch.equal(out[2], w)
     assert tq.device_status() == 0
+
+
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("M,D,F,E,k", [(1, 512, 1024, 8, 2), (1, 1536, 6144, 8, 2), (4, 1024, 512, 6, 3), (9, 512, 512, 5, 3),
+                                       (40, 1024, 1536, 6, 2)])
+def test_non_finite_tokens(cuda_lib, M, D, F, E, k, rms):
+    """A NaN or an infinity makes its own token's output NaN, as in the definition, and no other's; in a token without
+    used slots nobody looks at it."""
+    tq = cuda_lib
+    x, router, layers = make(M + D, M, D, F, E, True)
+    _, ids, w = tq.moe_swiglu(x, router, *layers, k, per_row=True, rmsnorm=rms)
+    x[0, D - 5] = float("nan")
+    if M > 2:
+        x[M - 1, 3] = float("inf")
+        x[1], ids[1] = float("nan"), -1
+    fl = tq.FLAG_FWHT | tq.GAMMA_PER_ROW | (tq.FLAG_RMSNORM if rms else 0)
+    y = torch.empty_like(x)
+    ws = torch.empty(tq.moe_workspace_bytes(M, D, F, E, k, fl), dtype=torch.uint8, device="cuda")
+    tq.moe_swiglu_(x, None, *layers, fl, y, ids, w, ws)
+    ref, mag, _, _ = reference(x, None, layers, k, True, rms, False, 0, ids=ids.long(), w=w)
+    bad = [0] if M <= 2 else [0, M - 1]
+    assert torch.isnan(ref[bad]).all() and torch.isnan(y[bad]).all()
+    rest = [m for m in range(M) if m not in bad]
+    if rest:
+        check_y(y[rest], ref[rest], mag[rest], k)
+        assert not y[1].any()
+    # with the router: its logits are NaN, and so are the weights
+    y, _, w = tq.moe_swiglu(x, router, *layers, k, per_row=True, rmsnorm=rms)
+    assert torch.isnan(y[bad]).all() and torch.isnan(w[bad]).all()
+    assert tq.device_status() == 0
+
+
+@pytest.mark.parametrize("M", [2, 30])
+def test_non_finite_scales(cuda_lib, M):
+    """A NaN scale of one row of an expert's gate: NaN for the tokens that chose the expert, or, sanitized, a zero."""
+    tq = cuda_lib
+    D, F, E, k = 512, 1024, 6, 2
+    x, router, layers = make(M, M, D, F, E, True)
+    want, ids, _ = tq.moe_swiglu(x, router, *layers, k, per_row=True)
+    e = int(ids[0, 0])
+    layers[0][1][e, 7] = float("nan")
+    y, _, _ = tq.moe_swiglu(x, router, *layers, k, per_row=True)
+    hit = (ids == e).any(1)
+    assert torch.isnan(y[hit]).all() and torch.equal(y[~hit], want[~hit])
+    y, _, _ = tq.moe_swiglu(x, router, *layers, k, per_row=True, sanitize=True)
+    layers[0][1][e, 7] = 0.0
+    assert torch.equal(y, tq.moe_swiglu(x, router, *layers, k, per_row=True, sanitize=True)[0])
+    assert tq.device_status() == 0
