@@ -39,14 +39,15 @@ __device__ __forceinline__ Fp8Scale fp8_block_scale(float amax) {
 // the IBM RISC System/6000 processor" (1990): a quotient within one unit, here v inv
 // corrected once, becomes the correctly rounded one by its exact remainder times
 // the correctly rounded reciprocal.  The remainders of quotients near a rounding
-// border of e4m3 are normal numbers (the floor of s).  A first quotient of zero stands,
-// for its sign, which the correction of a -0 would lose: v is zero or too small for any
-// code but zero, or s infinite, inv = 0, and v * 0 what v / s would be.
+// border of e4m3 are normal numbers (the floor of s).  The remainders are taken with
+// the opposite sign, q s - v, so that a quotient of -0 stays one: v = -0 leaves +0, and
+// -0 + (-0) inv is -0, where -0 + (+0) inv would be +0.  An infinite s has inv = 0,
+// and v * 0 is what v / s would be.
 __device__ __forceinline__ float fp8_quotient(float v, Fp8Scale k) {
     const float q0 = __fmul_rn(v, k.inv);
-    const float q1 = __fmaf_rn(__fmaf_rn(-q0, k.s, v), k.inv, q0);
-    const float q2 = __fmaf_rn(__fmaf_rn(-q1, k.s, v), k.inv, q1);
-    return q0 == 0.0f ? q0 : q2;
+    const float q1 = __fmaf_rn(-__fmaf_rn(q0, k.s, -v), k.inv, q0);
+    const float q2 = __fmaf_rn(-__fmaf_rn(q1, k.s, -v), k.inv, q1);
+    return k.inv == 0.0f ? q0 : q2;
 }
 
 // Codes of four quotients, lowest address first.

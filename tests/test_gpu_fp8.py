@@ -330,3 +330,34 @@ def test_padding_of_rows_without_a_finite_norm(cuda_lib, C):
     assert not q.view(torch.uint8)[:, C:].any()
     assert torch.isnan(q[:2, :C].float()).all()
     assert torch.equal(q[2:].view(torch.uint8), tq.quantize_fp8(x[2:].clone(), rmsnorm=True, rms_eps=0.0)[0].view(torch.uint8))
+
+
+def test_quantize_infinite_scale(cuda_lib):
+    """An infinity's block has an infinite scale in every form and its finite elements codes of 0 with their signs."""
+    tq = cuda_lib
+    x = normal(12, 140, 300)
+    x[5, 7], x[130, 299] = float("inf"), -float("inf")
+
+    def check(q, s, v, rows):
+        R, C = v.shape
+        want = torch.zeros(up(R, rows) // rows, up(C, 128) // 128, dtype=torch.bool, device="cuda")
+        for r, c in torch.nonzero(torch.isinf(v)).tolist():
+            want[r // rows, c // 128] = True
+        assert torch.equal(torch.isinf(s), want)
+        in_block = want.repeat_interleave(rows, 0)[:R].repeat_interleave(128, 1)[:, :C]
+        code = q.view(torch.uint8)[:, :C].long()
+        finite = in_block & torch.isfinite(v)
+        assert torch.equal(code[finite], torch.where(torch.signbit(v[finite]), 0x80, 0))
+        assert torch.isnan(q[:, :C].float()[torch.isinf(v)]).all()
+        rq, _ = ref_quant(torch.where(in_block, torch.zeros_like(v), v), rows, 128)
+        assert torch.equal(code[~in_block], rq.long()[~in_block])
+        assert not q.view(torch.uint8)[:, C:].any()
+
+    q, s = tq.quantize_fp8(x)
+    check(q, s.t(), x, 1)
+    check(*tq.quantize_fp8(x, square=True), x, 128)
+    for square in (False, True):
+        q, s, qt, st = tq.quantize_fp8(x, square=square, transpose=True)
+        check(q, s if square else s.t(), x, 128 if square else 1)
+        check(qt, st if square else st.t(), x.t().contiguous(), 128 if square else 1)
+    assert tq.device_status() == 0
