@@ -161,15 +161,22 @@ __global__ void __launch_bounds__(kActThreads)
     }
     ss = block_sum_d<kActThreads>(ss, redd);
     const double r = __ddiv_rn(1.0, __dsqrt_rn(__dadd_rn(__ddiv_rn(ss, (double)C), (double)eps)));
+    if (!isfinite(r)) {
+        // A NaN in the row, or an empty row without an eps: every element is a NaN, which no
+        // maximum takes in.  Apart from the loop, where 0 r would make NaNs of the zeros
+        // past the row too, and a test for them cost 3 %.
+        for (int64_t c = threadIdx.x; c < ldq; c += kActThreads) q[row * ldq + c] = c < C ? 0x7f : 0;
+        for (int64_t b = threadIdx.x; b < (C + 127) / 128; b += kActThreads) s[b * R + row] = fp8_scale(0.0f);
+        return;
+    }
     for (int64_t b = 128 * warp; b < ldq; b += 128 * (kActThreads / 32)) {
         const int64_t c = b + 4 * lane;
         float4 v = fp8_load4<BF16, VEC>(x, row, C, c);
         float e[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            // past the row zeros stay zeros, whatever r is (infinite or NaN rows)
             const double g = gain && c + i < C ? (double)__ldg(gain + c + i) : 1.0;
-            e[i] = c + i < C ? __double2float_rn(__dmul_rn(__dmul_rn((double)e[i], r), g)) : 0.0f;
+            e[i] = __double2float_rn(__dmul_rn(__dmul_rn((double)e[i], r), g));
         }
         v = make_float4(e[0], e[1], e[2], e[3]);
         const Fp8Scale sc = fp8_block_scale(warp_max(abs_max4(v)));
