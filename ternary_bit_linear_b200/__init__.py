@@ -502,19 +502,41 @@ def selftest_wait_timeout(limit_ns: int, sleeping: bool = False, stream=None):
 
 
 # ---------------------------------------------------------------------------
-# Allocating conveniences (torch allocates; the kernels compute).
+# Allocating conveniences (torch allocates; the kernels compute).  With `stream`
+# the work runs there and the buffers are taken there; as for every call, the
+# inputs must be complete on that stream, and whoever reads the results on
+# another one waits for it.
 # ---------------------------------------------------------------------------
+
+def _under(stream, call, first, *args):
+    """`call` with `stream` current: its buffers then come from that stream's pool, so scratch
+    dropped on return is reused behind the kernels that work on it, and nothing that another
+    stream still works on is written.  The results are tied to the caller's stream too: what
+    it frees goes back once its own work is done."""
+    import torch
+
+    if first.device != stream.device:
+        raise ValueError(f"stream on {stream.device}, tensors on {first.device}")
+    here = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        out = call(first, *args)
+    for t in out if isinstance(out, tuple) else (out,):
+        t.record_stream(here)
+    return out
+
 
 def quantize_ternary_pack(w, per_row: bool, sanitize: bool = False, stream=None):
     import torch
 
+    if stream is not None:
+        return _under(stream, quantize_ternary_pack, w, per_row, sanitize)
     N, K = w.shape
     flags = (GAMMA_PER_ROW if per_row else 0) | (FLAG_SANITIZE_NONFINITE if sanitize else 0)
     packed = torch.empty((N, K // 4), dtype=torch.uint8, device=w.device)
     gamma = torch.empty((N if per_row else 1,), dtype=torch.float32, device=w.device)
     nws = pack_workspace_bytes(N, K, flags)
     ws = torch.empty((max(nws, 16),), dtype=torch.uint8, device=w.device) if nws else None
-    quantize_ternary_pack_(w, flags, packed, gamma, ws, stream)
+    quantize_ternary_pack_(w, flags, packed, gamma, ws)
     return packed, gamma
 
 
@@ -522,20 +544,24 @@ def quantize_act_int8(x, clamp_eta: bool = False, eta_min: float = 0.05, eta_max
                       sanitize: bool = False, stream=None):
     import torch
 
+    if stream is not None:
+        return _under(stream, quantize_act_int8, x, clamp_eta, eta_min, eta_max, sanitize)
     M, K = x.shape
     flags = (FLAG_ETA_CLAMP if clamp_eta else 0) | (FLAG_SANITIZE_NONFINITE if sanitize else 0)
     xq = torch.empty((M, K), dtype=torch.int8, device=x.device)
     s_x = torch.empty((M,), dtype=torch.float32, device=x.device)
     rowsum = torch.empty((M,), dtype=torch.int32, device=x.device)
-    quantize_act_int8_(x, flags, eta_min, eta_max, xq, s_x, rowsum, stream)
+    quantize_act_int8_(x, flags, eta_min, eta_max, xq, s_x, rowsum)
     return xq, s_x, rowsum
 
 
 def fwht512(x, normalize: bool = True, stream=None):
     import torch
 
+    if stream is not None:
+        return _under(stream, fwht512, x, normalize)
     y = torch.empty_like(x)
-    fwht512_(x, y, normalize, stream)
+    fwht512_(x, y, normalize)
     return y
 
 
@@ -543,10 +569,12 @@ def ternary_gemm(xq, s_x, rowsum, packed, gamma, per_row: bool, with_acc: bool =
                  stream=None):
     import torch
 
+    if stream is not None:
+        return _under(stream, ternary_gemm, xq, s_x, rowsum, packed, gamma, per_row, with_acc)
     M, N = xq.shape[0], packed.shape[0]
     y = torch.empty((M, N), dtype=torch.float32, device=xq.device)
     acc = torch.empty((M, N), dtype=torch.int32, device=xq.device) if with_acc else None
-    ternary_gemm_(xq, s_x, rowsum, packed, gamma, GAMMA_PER_ROW if per_row else 0, y, acc, stream)
+    ternary_gemm_(xq, s_x, rowsum, packed, gamma, GAMMA_PER_ROW if per_row else 0, y, acc)
     return (y, acc) if with_acc else y
 
 
@@ -556,6 +584,9 @@ def bitlinear_fused(x, packed, gamma, per_row: bool, rmsnorm: bool = True, fwht:
                     return_xq: bool = False, stream=None):
     import torch
 
+    if stream is not None:
+        return _under(stream, bitlinear_fused, x, packed, gamma, per_row, rmsnorm, fwht, rms_gain, rms_eps,
+                      clamp_eta, eta_min, eta_max, sanitize, return_xq)
     M, K = x.shape
     N = packed.shape[0]
     flags = ((GAMMA_PER_ROW if per_row else 0) | (FLAG_RMSNORM if rmsnorm else 0) |
@@ -565,8 +596,7 @@ def bitlinear_fused(x, packed, gamma, per_row: bool, rmsnorm: bool = True, fwht:
     ws = torch.empty((fused_workspace_bytes(M, K, flags),), dtype=torch.uint8, device=x.device)
     xq = torch.empty((M, K), dtype=torch.int8, device=x.device) if return_xq else None
     sx = torch.empty((M,), dtype=torch.float32, device=x.device) if return_xq else None
-    bitlinear_fused_(x, packed, gamma, flags, y, ws, rms_gain, rms_eps, eta_min, eta_max, xq, sx,
-                     stream)
+    bitlinear_fused_(x, packed, gamma, flags, y, ws, rms_gain, rms_eps, eta_min, eta_max, xq, sx)
     return (y, xq, sx) if return_xq else y
 
 
@@ -575,6 +605,8 @@ def moe_swiglu(x, router, gate, up, down, top_k: int, per_row: bool = False, rms
     """A mixture-of-experts layer for up to 64 tokens: (y, ids, weights)."""
     import torch
 
+    if stream is not None:
+        return _under(stream, moe_swiglu, x, router, gate, up, down, top_k, per_row, rmsnorm, norm_topk, sanitize, clamp_val)
     M, D = x.shape
     E, F = gate[0].shape[0], gate[0].shape[1]
     flags = (FLAG_FWHT | (GAMMA_PER_ROW if per_row else 0) | (FLAG_RMSNORM if rmsnorm else 0) |
@@ -583,7 +615,7 @@ def moe_swiglu(x, router, gate, up, down, top_k: int, per_row: bool = False, rms
     ids = x.new_empty((M, top_k), dtype=torch.int32)
     weights = x.new_empty((M, top_k))
     ws = x.new_empty((moe_workspace_bytes(M, D, F, E, top_k, flags),), dtype=torch.uint8)
-    moe_swiglu_(x, router, gate, up, down, flags, y, ids, weights, ws, clamp_val, stream)
+    moe_swiglu_(x, router, gate, up, down, flags, y, ids, weights, ws, clamp_val)
     return y, ids, weights
 
 
@@ -599,6 +631,8 @@ def quantize_fp8(x, square: bool = False, transpose: bool = False, rmsnorm: bool
     """(q, s) of x [R, C] (float32 or bfloat16), or (q, s, qt, st) with `transpose`."""
     import torch
 
+    if stream is not None:
+        return _under(stream, quantize_fp8, x, square, transpose, rmsnorm, rms_gain, rms_eps)
     R, C = x.shape
     rb, cb, ldq, ldt = (R + 127) // 128, (C + 127) // 128, (C + 15) // 16 * 16, (R + 15) // 16 * 16
     dev, f8, f32, bf16 = x.get_device(), torch.float8_e4m3fn, torch.float32, x.dtype is torch.bfloat16
@@ -609,7 +643,7 @@ def quantize_fp8(x, square: bool = False, transpose: bool = False, rmsnorm: bool
     if transpose:
         qt = _new((C, ldt), f8, x.device)
         st = _new((cb, rb) if square else (rb, C), f32, x.device)
-    _call("tq_quantize_fp8", dev, stream, _fit(x, torch.bfloat16 if bf16 else f32, (R, C), dev, "x"), R, C, flags,
+    _call("tq_quantize_fp8", dev, None, _fit(x, torch.bfloat16 if bf16 else f32, (R, C), dev, "x"), R, C, flags,
           None if rms_gain is None else _fit(rms_gain, f32, (C,), dev, "rms_gain"), rms_eps, q.data_ptr(), s.data_ptr(),
           qt.data_ptr() if transpose else None, st.data_ptr() if transpose else None)
     return (q, s, qt, st) if transpose else (q, s)
@@ -619,6 +653,8 @@ def fp8_gemm(xq, s_x, wq, s_w, K: int, w_rows: bool = False, bf16: bool = False,
     """y [M, N] of codes and scales as quantize_fp8 gives them (w: its square form, or with `w_rows` its row form)."""
     import torch
 
+    if stream is not None:
+        return _under(stream, fp8_gemm, xq, s_x, wq, s_w, K, w_rows, bf16)
     y = _new((xq.shape[0], wq.shape[0]), torch.bfloat16 if bf16 else torch.float32, xq.device)
-    fp8_gemm_(xq, s_x, wq, s_w, K, (FLAG_FP8_W_ROWS if w_rows else 0) | (FLAG_BF16_OUTPUT if bf16 else 0), y, stream)
+    fp8_gemm_(xq, s_x, wq, s_w, K, (FLAG_FP8_W_ROWS if w_rows else 0) | (FLAG_BF16_OUTPUT if bf16 else 0), y)
     return y
