@@ -1323,8 +1323,9 @@ size_t tq_fp8_row_bytes(int64_t K) { return K > 0 ? (size_t)round_up(K, 16) : 0;
 
 tq_status tq_quantize_fp8(const void *x, int64_t rows, int64_t cols, unsigned flags, const float *rms_gain,
                           float rms_eps, uint8_t *q, float *s, uint8_t *qt, float *st, tq_stream_t stream) {
-    if (!x || !q || !s || (qt != nullptr) != (st != nullptr)) return TQ_ERR_NULL;
+    // the shape first: an empty tensor has no address
     if (rows < 1 || cols < 1 || rows > kFp8MaxDim || cols > kFp8MaxDim) return TQ_ERR_SHAPE;
+    if (!x || !q || !s || (qt != nullptr) != (st != nullptr)) return TQ_ERR_NULL;
     if (flags & ~(TQ_FLAG_BF16_INPUT | TQ_FLAG_FP8_SQUARE | TQ_FLAG_RMSNORM)) return TQ_ERR_ARG;
     const bool rms = flags & TQ_FLAG_RMSNORM, square = flags & TQ_FLAG_FP8_SQUARE;
     if (rms && (square || qt)) return TQ_ERR_ARG;
@@ -1353,8 +1354,8 @@ tq_status tq_quantize_fp8(const void *x, int64_t rows, int64_t cols, unsigned fl
 
 tq_status tq_fp8_gemm(const uint8_t *xq, const float *s_x, const uint8_t *wq, const float *s_w, unsigned flags,
                       int64_t M, int64_t N, int64_t K, void *y, tq_stream_t stream) {
-    if (!xq || !s_x || !wq || !s_w || !y) return TQ_ERR_NULL;
     if (M < 1 || N < 1 || K < 1 || M > kFp8MaxDim || N > kFp8MaxDim || K > kFp8MaxDim) return TQ_ERR_SHAPE;
+    if (!xq || !s_x || !wq || !s_w || !y) return TQ_ERR_NULL;
     if (flags & ~(TQ_FLAG_FP8_W_ROWS | TQ_FLAG_BF16_OUTPUT | TQ_FLAG_ACCUMULATE | TQ_FLAG_WEIGHTS_STATIC)) return TQ_ERR_ARG;
     const bool rows = flags & TQ_FLAG_FP8_W_ROWS, bf16 = flags & TQ_FLAG_BF16_OUTPUT;
     if (bf16 && (flags & TQ_FLAG_ACCUMULATE)) return TQ_ERR_ARG;
@@ -1391,10 +1392,11 @@ tq_status tq_moe_swiglu(const float *x, int64_t M, int64_t d_model, int64_t d_ff
                         const float *gate_gamma, const uint8_t *up_packed, const float *up_gamma,
                         const uint8_t *down_packed, const float *down_gamma, float *y, int32_t *expert_ids,
                         float *expert_weights, void *workspace, size_t workspace_bytes, tq_stream_t stream) {
+    // the shape first: the workspace of a refused one has 0 bytes, and so no address
+    if (!moe_shape_ok(M, d_model, d_ffn, n_experts, top_k)) return TQ_ERR_SHAPE;
     if (!x || !gate_packed || !gate_gamma || !up_packed || !up_gamma || !down_packed || !down_gamma || !y ||
         !expert_ids || !expert_weights || !workspace)
         return TQ_ERR_NULL;
-    if (!moe_shape_ok(M, d_model, d_ffn, n_experts, top_k)) return TQ_ERR_SHAPE;
     const unsigned known = TQ_GAMMA_PER_ROW | TQ_FLAG_FWHT | TQ_FLAG_RMSNORM | TQ_FLAG_SANITIZE_NONFINITE |
                            TQ_FLAG_WEIGHTS_STATIC | TQ_FLAG_NORM_TOPK | TQ_ENC_MASK;
     const int enc = flag_encoding(flags);

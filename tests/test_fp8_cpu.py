@@ -89,3 +89,11 @@ def test_binding_checks_tensors():
     x = torch.zeros(4, 32)
     with pytest.raises(ValueError):   # no CPU path
         tq.quantize_fp8(x)
+
+
+def test_an_empty_matrix_is_a_refused_shape(lib):
+    """Empty tensors have no address: the shape is what is wrong."""
+    assert lib.tq_quantize_fp8(None, 0, 64, 0, None, 1e-6, None, None, None, None, None) == SHAPE
+    assert lib.tq_quantize_fp8(None, 64, 0, 0, None, 1e-6, None, None, None, None, None) == SHAPE
+    for shape in ((0, 64, 64), (64, 0, 64), (64, 64, 0)):
+        assert lib.tq_fp8_gemm(None, None, None, None, 0, *shape, None, None) == SHAPE

@@ -83,3 +83,11 @@ def test_binding_checks_tensors():
     pack = (torch.zeros(2, 512, 128, dtype=torch.uint8), torch.zeros(2))
     with pytest.raises(ValueError):   # no CPU path
         tq.moe_swiglu(x, torch.zeros(2, 512), pack, pack, pack, 1)
+
+
+@pytest.mark.parametrize("name,value", BAD_SHAPES)
+def test_a_refused_shape_is_named_whatever_its_buffers(lib, name, value):
+    """The scratch of a refused shape has 0 bytes and no address; empty tensors have none either."""
+    call = caller(lib)
+    assert call(**{name: value}, ws=None, wsb=0) == SHAPE
+    assert call(**{name: value}, ws=None, wsb=0, x=None, y=None, ids=None, w=None) == SHAPE
