@@ -361,3 +361,43 @@ def test_quantize_infinite_scale(cuda_lib):
         check(q, s if square else s.t(), x, 128 if square else 1)
         check(qt, st if square else st.t(), x.t().contiguous(), 128 if square else 1)
     assert tq.device_status() == 0
+
+
+@pytest.mark.parametrize("M,N,K,bf16", [(40, 50, 60, False), (257, 384, 300, True), (1000, 640, 1100, False)])
+def test_gradients_against_the_formula(cuda_lib, M, N, K, bf16):
+    """dx and dw against the exact gradients of <dy, x w^T>, and along the steepest direction against its differences.
+
+    Bound, derived: rounding to e4m3 moves each of a term's two factors by at most 2^-4 of its value (elements with
+    subnormal codes by 2^-10 / 448 of their block's largest, which is nothing beside the block's mean square), so an
+    independent term's squared error is at most (2 * 2^-8 + 2^-16) of its square.  The operands are independent and of
+    mean zero, and so are the errors: the squared 2-norms of gradient and error are their terms' sums, and the error's
+    norm is at most sqrt(2) 2^-4 = 0.088 of the gradient's, plus their fluctuation, 1 / sqrt of the 2400 and more elements."""
+    tq = cuda_lib
+    x, w, dy = normal(21, M, K), 0.05 * normal(22, N, K), 0.001 * normal(23, M, N)
+    if bf16:
+        x, dy = x.bfloat16(), dy.bfloat16()
+    _, _, xt, sxt = tq.quantize_fp8(x, transpose=True)
+    dq, sd, dt, sdt = tq.quantize_fp8(dy, transpose=True)
+    _, _, wt, swt = tq.quantize_fp8(w, square=True, transpose=True)
+    dx = tq.fp8_gemm(dq, sd, wt, swt, N).double().cpu()
+    dw = tq.fp8_gemm(dt, sdt, xt, sxt, M, w_rows=True).double().cpu()
+    assert tq.device_status() == 0
+    X, W, D = x.double().cpu(), w.double().cpu(), dy.double().cpu()
+
+    def loss(X, W):
+        return (D * (X @ W.t())).sum()
+
+    bound = 2 ** 0.5 * 2.0 ** -4 * (1 + 2400 ** -0.5)
+    for grad, exact, at in ((dx, D @ W, 0), (dw, D.t() @ X, 1)):
+        size = exact.norm()
+
+        def off(g):
+            return (g - exact).norm() / size
+
+        assert off(grad) <= bound
+        # the bound is one: none of these keeps it
+        for wrong in (torch.zeros_like(grad), -grad, 1.2 * grad, grad.roll(1, 0), grad.roll(1, 1)):
+            assert off(wrong) > bound
+        u = exact / size
+        d = loss(X + u, W) - loss(X - u, W) if at == 0 else loss(X, W + u) - loss(X, W - u)  # the loss is linear in each
+        assert abs((grad * u).sum() - d / 2) <= bound * size and bound * size < 0.1 * d / 2
