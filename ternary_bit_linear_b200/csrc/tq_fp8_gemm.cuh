@@ -489,15 +489,15 @@ struct Fp8WideLayout {
     // 216 <= 384 x 168).
     static constexpr bool kMoveRegs = kCols > 64;
     static constexpr int kAccBufs = BN > 128 ? 2 : 4;
-    static constexpr int kDStride = BN > 128 ? 256 : BN;  // TMEM columns from buffer to buffer
-    static constexpr uint32_t kTmemCols = kAccBufs * kDStride;
+    static constexpr uint32_t kTmemCols = kAccBufs * BN;
     static constexpr int kA = 128 * kFp8Step, kB = BN * kFp8Step, kStage = kA + kB;
-    static constexpr int kStages = BN <= 128 ? 6 : BN <= 192 ? 5 : 4;
+    static constexpr int kStages = BN > 128 ? 4 : 6;
     static constexpr int offBar = kStages * kStage;
     static constexpr int kBars = 2 * kStages + 2 * kAccBufs + 1;
     static constexpr int offTmem = offBar + kBars * 8;
     static constexpr int kBytes = offTmem + 16;
     static constexpr int kDynamic = kBytes + 1024;
+    static_assert(BN == 128 || BN == 256, "an epilogue warp's columns lie in one block of w's scales");
     static_assert(kTmemCols <= 512 && kDynamic <= 232448 && kStage % 1024 == 0, "tensor and shared memory");
 };
 
@@ -648,7 +648,7 @@ __global__ void __launch_bounds__(Fp8WideLayout<BN>::kThreads, 1)
                 const uint32_t xa = sbase + (uint32_t)(s * L::kStage), wa = xa + L::kA;
 #pragma unroll
                 for (int k = 0; k < kFp8Step / 32; ++k)
-                    mma_f8(tmem + (uint32_t)(b * L::kDStride), smem_desc_sw128(xa + 32 * k),
+                    mma_f8(tmem + (uint32_t)(b * BN), smem_desc_sw128(xa + 32 * k),
                            smem_desc_sw128(wa + 32 * k), idesc, k != 0 ? 1u : 0u);
                 mma_commit(empty(s));
                 mma_commit(d_full(b));
@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(Fp8WideLayout<BN>::kThreads, 1)
 #pragma unroll
                 for (int f = 0; f < L::kInFlight; ++f)
                     tmem_ld_frag(lane_addr + ((uint32_t)(16 * ((f0 + f) & 1)) << 16) +
-                                     (uint32_t)(b * L::kDStride + 32 * ((f0 + f) >> 1)), r[f]);
+                                     (uint32_t)(b * BN + 32 * ((f0 + f) >> 1)), r[f]);
 #pragma unroll
                 for (int f = 0; f < L::kInFlight; ++f) tmem_ld_wait_for(r[f]);
 #pragma unroll

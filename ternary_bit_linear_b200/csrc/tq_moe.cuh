@@ -578,7 +578,7 @@ template <bool GATE, bool CONV, int PD>
 __device__ __forceinline__ void moe_contract(const MoeArgs &a, const MoeShared &sm, MoeRun &run, uint32_t ring, uint32_t x_s,
                                              int *red) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int ks = run.ks, team = run.team, kw = run.kw, T = kMoeWarps >> run.lg, spp = run.spp;
+    const int team = run.team, kw = run.kw, T = kMoeWarps >> run.lg, spp = run.spp;
     const int g = lane >> 2, t = lane & 3;
     const int K = GATE ? a.D : a.F, N = GATE ? a.F : a.D, XS = gemv_x_stride(K);
     const uint32_t xsw = (uint32_t)(t & 2) << 4;
