@@ -390,7 +390,8 @@ TQ_API size_t tq_swiglu_workspace_bytes(int64_t M, int64_t d_model, int64_t d_ff
  *
  *   x          [M][d_model] fp32.  1 <= M <= 64; d_model, d_ffn multiples of 512,
  *              at most 8192; 1 <= n_experts <= 256; top_k <= 16, n_experts.  For
- *              more tokens, tq_swiglu_mlp per expert.
+ *              more tokens, tq_swiglu_mlp per expert on the tokens that chose it,
+ *              gathered and added up by the caller.
  *   router     [n_experts][d_model] fp32, or NULL: expert_ids and expert_weights
  *              are then inputs.  An id outside [0, n_experts) marks an unused slot (a
  *              padded token, an expert of another rank): it adds nothing, and a
@@ -472,7 +473,9 @@ TQ_API size_t tq_fp8_row_bytes(int64_t K);
  *   flags     the above and TQ_FLAG_WEIGHTS_STATIC (see "Launch overlap").
  *   Shapes: 1 <= M, N, K <= 2^24.
  * A block's products (exact) and the blocks' scaled sums are added in fp32; the
- * result is a function of the arguments alone (no atomics).  For the layer
+ * result is a function of the arguments alone (no atomics).  The product of a
+ * block's two scales is an fp32 number: scales whose product is below 2^-126 lose
+ * bits, or the block, and above 2^128 give infinities or NaN.  For the layer
  * y = x w^T of a training step with x [M][K], w [N][K], dy [M][N]:
  *   y  = (x rows)  . (w square)          K  = K
  *   dx = (dy rows) . (w square)^T        the square form's qt, st;  K = N

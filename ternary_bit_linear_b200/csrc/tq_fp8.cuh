@@ -9,8 +9,10 @@
 // gradients), 128 x 1 down a column with the codes written transposed (the
 // operands of a contraction over rows), or 128 x 128 (weights).
 //
-// All forms read x once and are bound by memory: 5 bytes of traffic per fp32
-// element (3 per bf16 element), one more with the transposed codes.
+// All forms read x once (after RMSNorm twice, the second time from cache).  The least
+// traffic is 5 bytes per fp32 element (3 per bf16 element), one more with the transposed
+// codes; fp32 rows and 128 x 128 blocks come near the time of it, the others are held
+// up by their instructions, which a bf16 element does not halve.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -100,8 +102,8 @@ __device__ __forceinline__ float4 fp8_load4(const void *x, int64_t row, int64_t 
 // ---------------------------------------------------------------------------
 // 1 x 128 blocks.  One warp takes 512 columns of one row: four blocks, each of
 // its lanes four consecutive elements of each, so a block's maximum is one
-// warp reduction and its 128 codes one coalesced store.  11008 x 4096 fp32:
-// 36.6 us, 6.2 TB/s.
+// warp reduction and its 128 codes one coalesced store.  11008 x 4096 fp32: 36 us,
+// 6.2 TB/s; bf16: 34 us, 4.0 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kFp8RowWarps = 8;
 
@@ -140,7 +142,9 @@ __global__ void __launch_bounds__(32 * kFp8RowWarps)
 
 // The same after RMSNorm (x * rsqrt(mean x^2 + eps) * gain, the sum in fp64,
 // the product rounded once to fp32 as the fused layer's prologue does): one
-// CTA per row, the row read a second time from cache.
+// CTA per row, the row read a second time from cache.  2048 x 4096 bf16: 16.7 us;
+// 11008 x 4096 fp32: 77 us, 2.9 TB/s: two chains of fp64 operations with a reduction over
+// the CTA between them.
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kActThreads)
     tq_fp8_rows_norm_kernel(const void *__restrict__ x, int64_t R, int64_t C, int64_t ldq,
@@ -193,9 +197,11 @@ __global__ void __launch_bounds__(kActThreads)
 // column's meets in shared memory, and a thread's 16 rows of one column are
 // 16 consecutive bytes of the transposed codes, which pass through shared
 // memory to leave in whole 128-byte rows.  Three tiles per SM, so that one's loads
-// run while another's maxima meet.  11008 x 4096 fp32 to 128 x 128 blocks: 43.6 us,
-// with the transpose 44.9 us (6.0 TB/s); rows and columns, whose scales differ,
-// 60.6 us, each code twice from its own quotient.
+// run while another's maxima meet; of the 80 registers that leaves a thread, most forms
+// spill some (up to 104 bytes, 260 where cols % 4 != 0).  11008 x 4096 to 128 x 128
+// blocks: fp32 43.1 us, bf16 48.9 us; with the transpose 44.1 us (6.1 TB/s) and
+// 58.9 us; rows and columns, whose scales differ, 60.4 us and 65.4 us, each code twice
+// from its own quotient (issue slots 64 % busy).  11008 x 4094: 49 to 107 us.
 // ---------------------------------------------------------------------------
 template <bool BF16, bool VEC, bool SQUARE, bool TRANS>
 __global__ void __launch_bounds__(256, 3)
@@ -240,7 +246,7 @@ __global__ void __launch_bounds__(256, 3)
             *reinterpret_cast<float4 *>(&red[warp][4 * lane]) = m;
         }
         // A row's maximum over the 32 lanes: halving exchanges leave row lane / 2's in
-        // every lane (31 shuffles, not 80), which makes that row's scale for all.
+        // every lane (16 shuffles, not 80), which makes that row's scale for all.
         Fp8Scale mine{0.0f, 0.0f};
         if (!SQUARE) {
             float m[16];

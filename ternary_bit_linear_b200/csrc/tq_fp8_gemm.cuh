@@ -20,7 +20,7 @@
 //               step % kAccBufs and commits twice: the operand slot is free,
 //               the buffer is full.
 //   warp 2      scales: asynchronous copies of s_x[b][m0 ..] and s_w into a ring of
-//               eight steps (one load from L2 takes longer than a step).
+//               six or eight steps (one load from L2 takes longer than a step).
 //   warps 4 ..  epilogue: 4 warps per 64 tokens (one per TMEM lane quarter),
 //               a thread per row with its tokens' sums in registers; adding
 //               a block takes a multiplication of scales and a multiply-add each.
@@ -32,8 +32,10 @@
 // depend on timing.
 //
 // What bounds it: w for few tokens (16 x 32000 x 4096: 23.9 us, 5.6 TB/s; 1 x 4096 x
-// 4096, a latency, 6.2 us), the scales' traffic through shared memory for many, which
-// a kernel of its own avoids (tq_fp8_gemm_wide_kernel).
+// 4096, a latency, 6.3 us), for many the epilogue, whose products each meet a scale from
+// shared memory (scales per row of w, 5632 x 2048 x 2048: 49.7 us, issue slots 51 %
+// busy, the tensor pipe 22 %); with one scale per block of w a kernel of its own does
+// without (tq_fp8_gemm_wide_kernel).
 //
 // Every mbarrier wait is bounded (see mbar_wait); after a timeout the kernel
 // skips the remaining work, lets its copies and MMAs end and frees its tensor
@@ -194,7 +196,7 @@ struct Fp8Layout {
     static constexpr int offScale = kStages * kStage;
     static constexpr int kScales = BT + kFp8TileN;  // a slot: the tokens' scales, then w's (ROWS: 128, else one)
     static constexpr int offBar = offScale + kScaleSlots * kScales * 4;
-    // barriers: full[S], empty[S], d_full[A], d_empty[A], s_full[8], s_empty[8], mma_done
+    // barriers: full, empty [kStages], d_full, d_empty [kAccBufs], s_full, s_empty [kScaleSlots], mma_done
     static constexpr int kBars = 2 * kStages + 2 * kAccBufs + 2 * kScaleSlots + 1;
     static constexpr int offTmem = offBar + kBars * 8;
     static constexpr int kBytes = offTmem + 16;
@@ -469,10 +471,13 @@ __global__ void __launch_bounds__(Fp8Layout<BT>::kThreads, Fp8Layout<BT>::kCtas)
 // and the scale of a block of w is one for all columns of a warp.  They come
 // straight from L2, two steps ahead: a lane loads one token's, and shuffles spread
 // them (a shared ring filled by a warp of its own cost a third of the kernel's time
-// in barrier traffic).  2048 x 11008 x 4096: 114 us, 1.62 PFLOP/s (the narrow kernel:
-// 171 us); 4096 x 8192 x 8192: 298 us, 1.84 PFLOP/s.  The MMAs alone would take
-// 40 % of that: each step's operands, 48 KB, are written to and read from
-// shared memory, and its 128 KB of sums read from tensor memory.
+// in barrier traffic).  2048 x 11008 x 4096: 113 us, 1.63 PFLOP/s (the narrow kernel:
+// 171 us); 4096 x 8192 x 8192: 300 us, 1.83 PFLOP/s.  The MMAs alone would take
+// 40 % of that, and no pipe is full (2048 x 4096 x 4096: tensor 38 %, issue slots 39 %,
+// DRAM 6 %): a step is a chain of its MMAs, the epilogue's rounds of tensor-memory
+// loads, each waited for (the first stall), and the buffer's way back, of which two
+// buffers overlap one step.  Adding to y (accumulate) takes twice as long, 222 us at
+// 2048 x 11008 x 4096: its reads of y come after the sums, between the stores.
 //
 //   warp 0  producer   warp 1  TMEM, MMAs
 //   warps 4-11  epilogue, four warps per half of the columns; TMEM lane quarter = warp % 4

@@ -14,10 +14,13 @@
 // in fp64 and rounded once to fp32, so that the int8 codes that follow do not
 // hang on the last bits of an exponential.
 //
-// What bounds it: the packed weights of the chosen experts, read once (3 D F / 4
-// bytes each); for one or two tokens, the chain of dependent steps.  One token of
-// 512 x 1024, 2 of 8 experts: 14.6 us.  64 tokens of 2048 x 1536, 8 of 128 experts:
-// 94.6 us (302 MB, 3.2 TB/s over all).
+// The least it could take is the time of the chosen experts' packed weights, read once
+// (3 D F / 4 bytes each).  What bounds it is the chain of dependent phases and the waits
+// between them: no pipe is full (64 tokens of 2048 x 1536, 8 of 128 experts: DRAM 41 %,
+// issue slots 40 %, ALU 36 %; of 1536 x 6144, 2 of 8: 12, 34, 30 %), and the first stall
+// is a barrier.  One token of 512 x 1024, 2 of 8 experts: 14.6 us.  64 tokens of 2048 x
+// 1536, 8 of 128 experts: 94.9 us (302 MB, 3.2 TB/s over all).  With the choice given:
+// 13.4 and 84.7 us.
 //
 //   tq_moe_route_kernel: a CTA per token quantises it; the other CTAs compute the
 //     logits of 8 experts and four tokens each.
@@ -43,7 +46,7 @@
 //   and into the down phase from before the rotation; a lane reads only what it
 //   copied itself, so the ring needs no barrier.  They are
 //   contracted with mma.sync (u8 codes x s8), whose rate is no bound here; the logic
-//   operations that spread the codes are, at half the rate of the others, which is
+//   operations that spread the codes run at half the rate of the others, which is
 //   why a code stays where it is in its byte: field j is masked in place, counts
 //   4^j-fold and has sums of its own.  (Spreading them to fp16 for the twice as wide
 //   fp16 mma.sync took more of them: 149 us instead of 127 at 64 x 2048 x 1536 of

@@ -8,8 +8,9 @@ Training kernels: bwd (input gradient, dY [M][N] against the packed [N][K]),
 ste and flip (latent weights / gradient [N][K]).
 
 moe: a mixture-of-experts layer of --G experts, --topk of them per token (d_model K,
-d_ffn N).  fp8: block-scaled e4m3 product of M tokens with [N][K]; quant: its
-weight quantisation with the transpose.
+d_ffn N).  fp8: block-scaled e4m3 product of M tokens with [N][K], fp8_rows with
+scales per row of w; quant: its weight quantisation with the transpose, quant_rows
+that of activations [N][K] with the transpose.
 
 Inputs are random device tensors of the workloads' distributions (values do
 not affect timing); every call goes through the C ABI.  Exits non-zero if a
@@ -28,7 +29,7 @@ def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--kernel", required=True,
                     choices=["pack_row", "pack_tensor", "act", "fwht", "gemv", "gemm", "grouped", "fused", "bwd", "ste",
-                             "flip", "moe", "fp8", "quant"])
+                             "flip", "moe", "fp8", "fp8_rows", "quant", "quant_rows"])
     ap.add_argument("--G", type=int, default=8, help="layers per grouped call")
     ap.add_argument("--M", type=int, default=8)
     ap.add_argument("--N", type=int, default=4096)
@@ -77,17 +78,21 @@ def main():
         my, mids = torch.empty_like(X), torch.empty((M, a.topk), dtype=torch.int32, device=dev)
         mwt = torch.empty((M, a.topk), device=dev)
         mws = torch.empty((tq.moe_workspace_bytes(M, D, F, E, a.topk, mfl),), dtype=torch.uint8, device=dev)
-    if a.kernel in ("fp8", "quant"):
+    if a.kernel in ("fp8", "fp8_rows", "quant", "quant_rows"):
         x8, x8s = tq.quantize_fp8(X)
-        w8 = tq.quantize_fp8(W, square=True, transpose=True)
+        w8 = tq.quantize_fp8(W, square=not a.kernel.endswith("_rows"), transpose=True)
     torch.cuda.synchronize()
     for _ in range(a.reps):
         if a.kernel == "moe":
             tq.moe_swiglu_(X, router, mgate, mup, mdown, mfl, my, mids, mwt, mws)
         elif a.kernel == "fp8":
             tq.fp8_gemm_(x8, x8s, w8[0], w8[1], K, 0, y)
+        elif a.kernel == "fp8_rows":
+            tq.fp8_gemm_(x8, x8s, w8[0], w8[1], K, tq.FLAG_FP8_W_ROWS, y)
         elif a.kernel == "quant":
             tq.quantize_fp8_(W, tq.FLAG_FP8_SQUARE, *w8)
+        elif a.kernel == "quant_rows":
+            tq.quantize_fp8_(W, 0, *w8)
         elif a.kernel in ("pack_row", "pack_tensor"):
             tq.quantize_ternary_pack_(W, flags, packed, gamma, pws)
         elif a.kernel == "act":
