@@ -91,3 +91,23 @@ def test_captured_on_the_given_stream(cuda_lib):
         torch.cuda.synchronize()
         assert same(out, want), name
     assert tq.device_status() == 0
+
+
+def test_captured_on_a_second_stream(cuda_lib):
+    """A branch of a graph: the call on another stream than the captured one, joined again, its results read there."""
+    tq = cuda_lib
+    for name, call, _ in calls(tq):
+        want = as_bytes(call(None))
+        torch.cuda.synchronize()
+        g, st, side = torch.cuda.CUDAGraph(), torch.cuda.Stream(), torch.cuda.Stream()
+        with torch.cuda.graph(g, stream=st):
+            side.wait_stream(st)
+            out = call(side)
+            st.wait_stream(side)
+            read = as_bytes(out)
+            del out
+        for _ in range(3):
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(read, want, strict=True)), name
+    assert tq.device_status() == 0
